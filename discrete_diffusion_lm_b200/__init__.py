@@ -10,7 +10,9 @@ the GPU, or the device is not sm_100, the calls raise.
 Functions carry the C ABI's names (include/dg.h):
     sampler:   dg_sampler_step, dg_sampler_selfcond_step, dg_sampler_step_eb,
                dg_entropy_accept, dg_adaptive_stop, dg_tau_linear, dg_sampler_step_noalloc
-    self-conditioning input:   dg_selfcond, dg_ffw
+    self-conditioning input:   dg_selfcond, dg_ffw, dg_ffw_mx4 (in 4 bits)
+    norms around a block:      dg_block_norm, dg_block_norm_backward
+    4-bit matrices (MXFP4):    dg_mx4_quantize, dg_mx4_dequantize, dg_mx4_matmul
     training:  dg_forward_noise, dg_canvas_ce, dg_canvas_ce_backward, dg_selfcond_drop
 plus the workspace-size queries, dg_last_error, dg_device_error, dg_launch_count, dg_version.
 
@@ -63,6 +65,7 @@ class DGError(RuntimeError):
 _lib = None
 _p, _i32, _i64, _u32, _u64, _sz, _int = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
                                          ctypes.c_uint64, ctypes.c_size_t, ctypes.c_int)
+_f32 = ctypes.c_float
 
 
 def lib() -> ctypes.CDLL:
@@ -107,6 +110,20 @@ def lib() -> ctypes.CDLL:
         L.dg_sampler_selfcond_step.argtypes = [_p, _int, _i64, _p, _i32, _i32, _i32, _int, _p, _p, _p, _u64, _u32,
                                                _int, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p, _int, _i32, _p, _p,
                                                _sz, _p]
+        L.dg_block_norm.argtypes = [_p, _i64, _p, _i64, _int, _p, _p, _p, _int, _i32, _i32, _i32, _f32, _f32, _p, _p,
+                                    _p, _p, _p]
+        L.dg_block_norm_backward_workspace_size.argtypes = [_i32, _i32, _i32, _int]
+        L.dg_block_norm_backward_workspace_size.restype = _sz
+        L.dg_block_norm_backward.argtypes = [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _int, _p, _p, _p, _int, _i32,
+                                             _i32, _i32, _f32, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]
+        L.dg_mx4_scale_bytes.argtypes = [_i32, _i32]
+        L.dg_mx4_scale_bytes.restype = _sz
+        L.dg_mx4_quantize.argtypes = [_p, _int, _i64, _i32, _i32, _p, _p, _p]
+        L.dg_mx4_dequantize.argtypes = [_p, _p, _i32, _i32, _p, _int, _p]
+        L.dg_mx4_matmul.argtypes = [_p, _p, _p, _p, _i32, _i32, _i32, _p, _int, _p]
+        L.dg_ffw_mx4_workspace_size.argtypes = [_i32, _i32, _i32]
+        L.dg_ffw_mx4_workspace_size.restype = _sz
+        L.dg_ffw_mx4.argtypes = [_p, _i32, _i32, _i32, _p, _p, _p, _p, _p, _p, _sz, _p]
         _lib = L
     return _lib
 
@@ -572,3 +589,306 @@ def dg_ffw(z: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, *, hidden: Optio
                       ws.numel() * ws.element_size(), _stream(stream))
     _check("dg_ffw", rc)
     return out, hidden
+
+
+# ------------------------------------------------------------------------------ the block around the FFW
+# These calls run on the device of their tensors, whichever is current, on `stream` or that device's
+# current stream; outputs and scratch that they allocate belong to the stream they run on.
+_DTYPE = {torch.float32: DG_F32, torch.bfloat16: DG_BF16}
+
+
+def _dtype_of(t: torch.Tensor, name: str) -> int:
+    code = _DTYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return code
+
+
+def _arg(t: torch.Tensor, name: str, dev: int, dtype, shape) -> int:
+    """Device address of a contiguous tensor argument of the given dtype and shape on device `dev`."""
+    if t.get_device() != dev:
+        _wrong_device(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows_arg(t: torch.Tensor, name: str, dev: int, dtype, shape):
+    """Device address and row stride of a 2-D tensor whose last dimension is contiguous."""
+    if t.get_device() != dev:
+        _wrong_device(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be of shape {list(shape)}, got {list(t.shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] != 1:
+        raise ValueError(f"{name} must have unit stride along the last dim")
+    return t.data_ptr(), (s0 if shape[0] > 1 else shape[1])
+
+
+def _wrong_device(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise ValueError("the library takes CUDA tensors only (got %s on %s)" % (name, t.device))
+    raise ValueError(f"{name} is on {t.device}, another device than the first argument")
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        _wrong_device(t, name)
+    return dev
+
+
+class _On:
+    """The device and stream that a call runs on, where they are not the current ones."""
+
+    def __init__(self, dev: int, stream):
+        self.parts = [torch.cuda.device(dev)] + ([torch.cuda.stream(stream)] if stream is not None else [])
+
+    def __enter__(self):
+        for p in self.parts:
+            p.__enter__()
+
+    def __exit__(self, *exc):
+        for p in reversed(self.parts):
+            p.__exit__(*exc)
+
+
+def _given(out: Optional[dict], key: str):
+    return None if out is None else out.get(key)
+
+
+def dg_block_norm(x: torch.Tensor, w_pre: Optional[torch.Tensor] = None, *, y: Optional[torch.Tensor] = None,
+                  w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, C: Optional[int] = None,
+                  res_scale: float = 1.0, eps: float = 1e-6, out: Optional[dict] = None, stream=None) -> dict:
+    """Norms after a block (y given: x + res_scale gate w_post n(y), key "x") and before the next
+    (w_pre given: w_pre n(stream), key "h"), with the reciprocal root means "rstd_y" and "rstd_x" that the
+    backward pass takes.  x, y: [B*C, d]; gate: [B, d], one row per canvas of C rows.  Pass `out` to
+    reuse buffers; out["x"] may be x itself."""
+    dev = _device_of(x, "x")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _On(dev, stream):
+            return dg_block_norm(x, w_pre, y=y, w_post=w_post, gate=gate, C=C, res_scale=res_scale, eps=eps, out=out)
+    dtype, shape = x.dtype, x.shape
+    act = _dtype_of(x, "x")
+    if len(shape) != 2:
+        raise ValueError("x must be a 2-D tensor")
+    R, d = shape
+    px, ld_x = _rows_arg(x, "x", dev, dtype, shape)
+    C = R if C is None else C
+    if C < 1 or R % C:
+        raise ValueError("rows must be a multiple of C")
+    given = w_pre if w_pre is not None else w_post
+    if given is None:
+        raise ValueError("w_pre or w_post (with y) is needed")
+    ptype, par = given.dtype, _dtype_of(given, "w_pre" if w_pre is not None else "w_post")
+    res = {}
+    py = pw = pg = pn = po = ph = pry = prx = None
+    ld_y = d
+    if y is not None:
+        if w_post is None:
+            raise ValueError("y needs w_post")
+        py, ld_y = _rows_arg(y, "y", dev, dtype, shape)
+        pw = _arg(w_post, "w_post", dev, ptype, (d,))
+        if gate is not None:
+            pg = _arg(gate, "gate", dev, ptype, (R // C, d))
+        res["x"] = o = _given(out, "x") if _given(out, "x") is not None else torch.empty(shape, dtype=dtype, device=x.device)
+        res["rstd_y"] = ry = _given(out, "rstd_y") if _given(out, "rstd_y") is not None else torch.empty(R, dtype=torch.float32, device=x.device)
+        po, pry = _arg(o, 'out["x"]', dev, dtype, shape), _arg(ry, 'out["rstd_y"]', dev, torch.float32, (R,))
+    elif w_post is not None or gate is not None:
+        raise ValueError("w_post and gate come only with y")
+    if w_pre is not None:
+        pn = _arg(w_pre, "w_pre", dev, ptype, (d,))
+        res["h"] = h = _given(out, "h") if _given(out, "h") is not None else torch.empty(shape, dtype=dtype, device=x.device)
+        res["rstd_x"] = rx = _given(out, "rstd_x") if _given(out, "rstd_x") is not None else torch.empty(R, dtype=torch.float32, device=x.device)
+        ph, prx = _arg(h, 'out["h"]', dev, dtype, shape), _arg(rx, 'out["rstd_x"]', dev, torch.float32, (R,))
+    rc = lib().dg_block_norm(px, ld_x, py, ld_y, act, pw, pg, pn, par, R // C, C, d, res_scale, eps, po, ph, pry, prx,
+                             torch.cuda.current_stream().cuda_stream)
+    if rc:
+        _check("dg_block_norm", rc)
+    return res
+
+
+def dg_block_norm_backward(dx_out: Optional[torch.Tensor], dh: Optional[torch.Tensor], x: torch.Tensor,
+                           w_pre: Optional[torch.Tensor] = None, *, rstd_x: Optional[torch.Tensor] = None,
+                           y: Optional[torch.Tensor] = None, w_post: Optional[torch.Tensor] = None,
+                           gate: Optional[torch.Tensor] = None, rstd_y: Optional[torch.Tensor] = None,
+                           C: Optional[int] = None, res_scale: float = 1.0, out: Optional[dict] = None,
+                           ws: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of dg_block_norm: dx_out of its stream (None: zero), dh of its h; x is the stream that h
+    was taken of (out["x"] of the forward call, or its x where it had no y).  Returns "dx" and, where
+    the call had them, "dw_pre" (w_pre), "dy", "dw_post" (y) and "dgate" (gate); the parameters'
+    gradients are float32."""
+    dev = _device_of(x, "x")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _On(dev, stream):
+            return dg_block_norm_backward(dx_out, dh, x, w_pre, rstd_x=rstd_x, y=y, w_post=w_post, gate=gate,
+                                          rstd_y=rstd_y, C=C, res_scale=res_scale, out=out, ws=ws)
+    dtype, shape = x.dtype, x.shape
+    act = _dtype_of(x, "x")
+    if len(shape) != 2:
+        raise ValueError("x must be a 2-D tensor")
+    R, d = shape
+    C = R if C is None else C
+    if C < 1 or R % C:
+        raise ValueError("rows must be a multiple of C")
+    given = w_pre if w_pre is not None else w_post
+    if given is None:
+        raise ValueError("w_pre or w_post (with y) is needed")
+    ptype, par = given.dtype, _dtype_of(given, "w_pre" if w_pre is not None else "w_post")
+    res, f32 = {}, torch.float32
+
+    def new(key, dt, shp):
+        t = _given(out, key)
+        res[key] = t = torch.empty(shp, dtype=dt, device=x.device) if t is None else t
+        return _arg(t, f'out["{key}"]', dev, dt, shp)
+
+    pdo = pdh = px = py = pw = pg = pn = pry = prx = pdy = pdw = pdg = pdn = None
+    ld_do = ld_dh = ld_x = ld_y = d
+    if dx_out is not None:
+        pdo, ld_do = _rows_arg(dx_out, "dx_out", dev, dtype, shape)
+    pdx = new("dx", dtype, shape)
+    if w_pre is not None:
+        if dh is None or rstd_x is None:
+            raise ValueError("w_pre needs dh and rstd_x")
+        px, ld_x = _rows_arg(x, "x", dev, dtype, shape)
+        pdh, ld_dh = _rows_arg(dh, "dh", dev, dtype, shape)
+        pn, prx = _arg(w_pre, "w_pre", dev, ptype, (d,)), _arg(rstd_x, "rstd_x", dev, f32, (R,))
+        pdn = new("dw_pre", f32, (d,))
+    elif dh is not None:
+        raise ValueError("dh comes only with w_pre")
+    if y is not None:
+        if w_post is None or rstd_y is None:
+            raise ValueError("y needs w_post and rstd_y")
+        py, ld_y = _rows_arg(y, "y", dev, dtype, shape)
+        pw, pry = _arg(w_post, "w_post", dev, ptype, (d,)), _arg(rstd_y, "rstd_y", dev, f32, (R,))
+        pdy, pdw = new("dy", dtype, shape), new("dw_post", f32, (d,))
+        if gate is not None:
+            pg = _arg(gate, "gate", dev, ptype, (R // C, d))
+            pdg = new("dgate", f32, (R // C, d))
+    elif w_post is not None or gate is not None:
+        raise ValueError("w_post and gate come only with y")
+    L = lib()
+    nbytes = L.dg_block_norm_backward_workspace_size(R // C, C, d, pg is not None)
+    if ws is None:
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the device of x")
+    rc = L.dg_block_norm_backward(pdo, ld_do, pdh, ld_dh, px, ld_x, py, ld_y, act, pw, pg, pn, par, R // C, C, d, res_scale,
+                                  pry, prx, pdx, pdy, pdw, pdg, pdn, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                  torch.cuda.current_stream().cuda_stream)
+    if rc:
+        _check("dg_block_norm_backward", rc)
+    return res
+
+
+def dg_mx4_scale_shape(rows: int, K: int) -> tuple:
+    """Shape of the scale bytes of a [rows, K] MXFP4 matrix: tiles of 128 rows x 4 blocks of 32."""
+    return (-(-rows // 128), -(-K // 128), 32, 16)
+
+
+def dg_mx4_quantize(x: torch.Tensor, *, out=None, stream=None):
+    """x [rows, K] (float32 or bfloat16) in MXFP4: (codes uint8 [rows, K/2], scales uint8 in the shape of
+    dg_mx4_scale_shape).  Pass out=(codes, scales) to reuse buffers."""
+    dev = _device_of(x, "x")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _On(dev, stream):
+            return dg_mx4_quantize(x, out=out)
+    shape = x.shape
+    dt = _dtype_of(x, "x")
+    if len(shape) != 2:
+        raise ValueError("x must be a 2-D tensor")
+    R, K = shape
+    px, ld = _rows_arg(x, "x", dev, x.dtype, shape)
+    u8, scale_shape = torch.uint8, dg_mx4_scale_shape(R, K)
+    if out is None:
+        codes, scales = torch.empty((R, K // 2), dtype=u8, device=x.device), torch.empty(scale_shape, dtype=u8, device=x.device)
+    else:
+        codes, scales = out
+    rc = lib().dg_mx4_quantize(px, dt, ld, R, K, _arg(codes, "codes", dev, u8, (R, K // 2)),
+                               _arg(scales, "scales", dev, u8, scale_shape), torch.cuda.current_stream().cuda_stream)
+    if rc:
+        _check("dg_mx4_quantize", rc)
+    return codes, scales
+
+
+def dg_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values [rows, K] that MXFP4 codes and scales stand for."""
+    dev = _device_of(codes, "codes")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _On(dev, stream):
+            return dg_mx4_dequantize(codes, scales, dtype=dtype, out=out)
+    if len(codes.shape) != 2:
+        raise ValueError("codes must be a 2-D tensor")
+    R, K = codes.shape[0], 2 * codes.shape[1]
+    u8 = torch.uint8
+    if out is None:
+        out = torch.empty((R, K), dtype=dtype, device=codes.device)
+    rc = lib().dg_mx4_dequantize(_arg(codes, "codes", dev, u8, codes.shape), _arg(scales, "scales", dev, u8, dg_mx4_scale_shape(R, K)),
+                                 R, K, _arg(out, "out", dev, dtype, (R, K)), _dtype_of(out, "out"),
+                                 torch.cuda.current_stream().cuda_stream)
+    if rc:
+        _check("dg_mx4_dequantize", rc)
+    return out
+
+
+def _mx4_arg(q, name: str, dev: int, rows: int, K: int):
+    codes, scales = q
+    return (_arg(codes, f"{name} codes", dev, torch.uint8, (rows, K // 2)),
+            _arg(scales, f"{name} scales", dev, torch.uint8, dg_mx4_scale_shape(rows, K)))
+
+
+def dg_mx4_matmul(a, w, *, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """a w^T [M, N] of two MXFP4 matrices a = (codes, scales) [M, K] and w [N, K], fp32 accumulation."""
+    dev = _device_of(a[0], "a codes")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _On(dev, stream):
+            return dg_mx4_matmul(a, w, dtype=dtype, out=out)
+    if len(a[0].shape) != 2 or len(w[0].shape) != 2:
+        raise ValueError("codes must be 2-D tensors")
+    M, K, N = a[0].shape[0], 2 * a[0].shape[1], w[0].shape[0]
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=a[0].device)
+    pa, psa = _mx4_arg(a, "a", dev, M, K)
+    pw, psw = _mx4_arg(w, "w", dev, N, K)
+    rc = lib().dg_mx4_matmul(pa, psa, pw, psw, M, N, K, _arg(out, "out", dev, dtype, (M, N)), _dtype_of(out, "out"),
+                             torch.cuda.current_stream().cuda_stream)
+    if rc:
+        _check("dg_mx4_matmul", rc)
+    return out
+
+
+def dg_ffw_mx4(z: torch.Tensor, w1, w2, *, out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """The feed-forward block gelu(z W1) W2 in MXFP4 (z bf16 [R, d], quantised by the call).  w1 = (codes,
+    scales) of W1 transposed, [d_ff, d]; w2 of W2 transposed, [d, d_ff]: for weights as dg_ffw takes them,
+    dg_mx4_quantize(W.t().contiguous())."""
+    dev = _device_of(z, "z")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _On(dev, stream):
+            return dg_ffw_mx4(z, w1, w2, out=out, ws=ws)
+    if len(z.shape) != 2:
+        raise ValueError("z must be a 2-D tensor")
+    R, d = z.shape
+    dff = w1[0].shape[0]
+    bf16 = torch.bfloat16
+    pz = _arg(z, "z", dev, bf16, (R, d))
+    p1, ps1 = _mx4_arg(w1, "w1", dev, dff, d)
+    p2, ps2 = _mx4_arg(w2, "w2", dev, d, dff)
+    if out is None:
+        out = torch.empty((R, d), dtype=bf16, device=z.device)
+    L = lib()
+    if ws is None:
+        ws = torch.empty(max(256, L.dg_ffw_mx4_workspace_size(R, d, dff)), dtype=torch.uint8, device=z.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous tensor on the device of z")
+    rc = L.dg_ffw_mx4(pz, R, d, dff, p1, ps1, p2, ps2, _arg(out, "out", dev, bf16, (R, d)), ws.data_ptr(),
+                      ws.numel() * ws.element_size(), torch.cuda.current_stream().cuda_stream)
+    if rc:
+        _check("dg_ffw_mx4", rc)
+    return out

@@ -168,6 +168,68 @@ int check_inv_tau(const float* inv_tau, int32_t B, float* out) {
     return DG_OK;
 }
 
+int check_norm_shape(int act_dtype, int param_dtype, int32_t B, int32_t C, int32_t d, float res_scale) {
+    if (!valid_dtype(act_dtype)) return fail(DG_ERR_INVALID_ARG, "activation dtype %d is not DG_F32 or DG_BF16", act_dtype);
+    if (!valid_dtype(param_dtype)) return fail(DG_ERR_INVALID_ARG, "parameter dtype %d is not DG_F32 or DG_BF16", param_dtype);
+    const int rc = check_canvases(B, C);
+    if (rc != DG_OK) return rc;
+    if (d < 8 || d > 16384 || d % 8 != 0) return fail(DG_ERR_INVALID_ARG, "d = %d must be a multiple of 8 in [8, 16384]", d);
+    if (!std::isfinite(res_scale)) return fail(DG_ERR_INVALID_ARG, "res_scale must be finite");
+    return DG_OK;
+}
+
+// Which norms a call has: y and w_post for the one after the block (with or without a gate), w_pre
+// for the one before the next.
+int check_norm_parts(const void* x, const void* y, const void* w_post, const void* gate, const void* w_pre) {
+    if (!x) return fail(DG_ERR_INVALID_ARG, "x is required");
+    if ((y != nullptr) != (w_post != nullptr)) return fail(DG_ERR_INVALID_ARG, "y and w_post come together");
+    if (gate && !y) return fail(DG_ERR_INVALID_ARG, "gate comes only with y");
+    if (!y && !w_pre) return fail(DG_ERR_INVALID_ARG, "neither y nor w_pre is given: nothing to compute");
+    return DG_OK;
+}
+
+int check_norm_rows(const char* name, const void* p, int64_t ld, int dtype, int32_t d) {
+    if (ld < d) return fail(DG_ERR_INVALID_ARG, "the row stride %lld of %s is smaller than d = %d", (long long)ld, name, d);
+    if (!aligned16(p) || (ld * elt_size(dtype)) % 16 != 0)
+        return fail(DG_ERR_ALIGNMENT, "%s: base and row stride must be multiples of 16 bytes", name);
+    return DG_OK;
+}
+
+// How the backward pass cuts the rows: runs of run_rows rows within a canvas, or within all rows
+// where no gate asks for sums per canvas.
+struct NormRuns {
+    int32_t B, C, runs, run_rows;
+};
+NormRuns norm_runs(int32_t B, int32_t C, bool have_gate) {
+    NormRuns n;
+    n.B = have_gate ? B : 1;
+    n.C = have_gate ? C : B * C;
+    const int32_t want = block_norm_runs(n.B, n.C);
+    n.run_rows = (n.C + want - 1) / want;
+    n.runs = (n.C + n.run_rows - 1) / n.run_rows;
+    return n;
+}
+
+int check_mx4_matrix(int32_t rows, int32_t K) {
+    if (rows < 1) return fail(DG_ERR_INVALID_ARG, "the row count %d must be >= 1", rows);
+    if (K < 32 || K % 32 != 0) return fail(DG_ERR_INVALID_ARG, "K = %d must be a positive multiple of 32", K);
+    return DG_OK;
+}
+
+// Workspace of the 4-bit feed-forward block: the quantised input and hidden layer.
+struct Mx4FfwParts {
+    size_t z_codes, z_scales, h_codes, h_scales, total;
+};
+Mx4FfwParts ffw_mx4_parts(int32_t rows, int32_t d, int32_t d_ff) {
+    Mx4FfwParts n;
+    n.z_codes = align_up(static_cast<size_t>(rows) * d / 2, 256);
+    n.z_scales = align_up(mx4_scale_bytes(rows, d), 256);
+    n.h_codes = align_up(static_cast<size_t>(rows) * d_ff / 2, 256);
+    n.h_scales = align_up(mx4_scale_bytes(rows, d_ff), 256);
+    n.total = n.z_codes + n.z_scales + n.h_codes + n.h_scales;
+    return n;
+}
+
 }  // namespace
 
 void note_launches(uint64_t n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
@@ -193,14 +255,15 @@ int dg_device_error(int* code) {
     if ((rc = check_device()) != DG_OK) return rc;
     const cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-    int c[4] = {0, 0, 0, 0};
+    int c[5] = {0, 0, 0, 0, 0};
     cudaError_t r = read_and_clear_device_error(&c[0]);
     if (r == cudaSuccess) r = read_and_clear_pass_error(&c[1]);
     if (r == cudaSuccess) r = read_and_clear_ops_error(&c[2]);
     if (r == cudaSuccess) r = read_and_clear_noise_error(&c[3]);
+    if (r == cudaSuccess) r = read_and_clear_mx4_error(&c[4]);
     if (r != cudaSuccess) return cuda_fail(r, "reading the device error words");
     *code = 0;
-    for (int k = 0; k < 4; ++k)  // the largest code: a failed check (2) before an expired wait (1)
+    for (int k = 0; k < 5; ++k)  // the largest code: a failed check (2) before an expired wait (1)
         if (c[k] > *code) *code = c[k];
     return DG_OK;
 }
@@ -748,6 +811,237 @@ int dg_ffw(const void* z_in, int32_t rows, int32_t d, int32_t d_ff, const void* 
         const cudaError_t e = launch_selfcond(sp, s);
         if (e != cudaSuccess) return cuda_fail(e, layer == 0 ? "FFW layer 1 launch" : "FFW layer 2 launch");
     }
+    return DG_OK;
+}
+
+
+int dg_block_norm(const void* x, int64_t ld_x, const void* y, int64_t ld_y, int act_dtype, const void* w_post,
+                  const void* gate, const void* w_pre, int param_dtype, int32_t B, int32_t C, int32_t d, float res_scale,
+                  float eps, void* x_out, void* h, float* rstd_y, float* rstd_x, dg_stream_t stream) {
+    g_last_error.clear();
+    int rc;
+    if ((rc = check_norm_shape(act_dtype, param_dtype, B, C, d, res_scale)) != DG_OK) return rc;
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(DG_ERR_INVALID_ARG, "eps = %g must be finite and >= 0", static_cast<double>(eps));
+    if ((rc = check_norm_parts(x, y, w_post, gate, w_pre)) != DG_OK) return rc;
+    if ((y != nullptr) != (x_out != nullptr)) return fail(DG_ERR_INVALID_ARG, "x_out is required with y, and only then");
+    if ((w_pre != nullptr) != (h != nullptr)) return fail(DG_ERR_INVALID_ARG, "h is required with w_pre, and only then");
+    if ((rc = check_norm_rows("x", x, ld_x, act_dtype, d)) != DG_OK) return rc;
+    if (y && (rc = check_norm_rows("y", y, ld_y, act_dtype, d)) != DG_OK) return rc;
+    if (!aligned16(w_post) || !aligned16(gate) || !aligned16(w_pre) || !aligned16(x_out) || !aligned16(h))
+        return fail(DG_ERR_ALIGNMENT, "w_post, gate, w_pre, x_out and h must be 16-byte aligned");
+    if (x_out && x_out == x && ld_x != d) return fail(DG_ERR_INVALID_ARG, "x_out may be x itself only where ld_x = d");
+    if ((x_out && x_out == y) || (h && (h == x || h == y || h == x_out)))
+        return fail(DG_ERR_INVALID_ARG, "x_out may not alias y, and h may not alias x, y or x_out");
+    if ((rc = check_device()) != DG_OK) return rc;
+    BlockNormParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = x;
+    p.y = y;
+    p.ld_x = ld_x;
+    p.ld_y = ld_y;
+    p.w_post = w_post;
+    p.gate = gate;
+    p.w_pre = w_pre;
+    p.R = B * C;
+    p.C = C;
+    p.d = d;
+    p.res_scale = res_scale;
+    p.eps = eps;
+    p.x_out = x_out;
+    p.h = h;
+    p.rstd_y = rstd_y;
+    p.rstd_x = rstd_x;
+    const cudaError_t e = launch_block_norm(p, act_dtype == DG_BF16, param_dtype == DG_BF16, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "block norm launch");
+    return DG_OK;
+}
+
+size_t dg_block_norm_backward_workspace_size(int32_t B, int32_t C, int32_t d, int have_gate) {
+    if (B < 1 || C < 1 || d < 1 || static_cast<long long>(B) * C > 0x7fffffffLL) return 0;
+    const NormRuns n = norm_runs(B, C, have_gate != 0);
+    return 2 * static_cast<size_t>(n.B) * n.runs * d * sizeof(float);
+}
+
+int dg_block_norm_backward(const void* dx_out, int64_t ld_dx_out, const void* dh, int64_t ld_dh, const void* x, int64_t ld_x,
+                           const void* y, int64_t ld_y, int act_dtype, const void* w_post, const void* gate,
+                           const void* w_pre, int param_dtype, int32_t B, int32_t C, int32_t d, float res_scale,
+                           const float* rstd_y, const float* rstd_x, void* dx, void* dy, float* dw_post, float* dgate,
+                           float* dw_pre, void* workspace, size_t workspace_bytes, dg_stream_t stream) {
+    g_last_error.clear();
+    int rc;
+    if ((rc = check_norm_shape(act_dtype, param_dtype, B, C, d, res_scale)) != DG_OK) return rc;
+    if ((rc = check_norm_parts(x ? x : dx_out, y, w_post, gate, w_pre)) != DG_OK) return rc;
+    if (!dx) return fail(DG_ERR_INVALID_ARG, "dx is required");
+    if (w_pre && (!dh || !x || !rstd_x || !dw_pre)) return fail(DG_ERR_INVALID_ARG, "w_pre needs dh, x, rstd_x and dw_pre");
+    if (!w_pre && (dh || dw_pre)) return fail(DG_ERR_INVALID_ARG, "dh and dw_pre come only with w_pre");
+    if (!w_pre && !dx_out) return fail(DG_ERR_INVALID_ARG, "dx_out is required without w_pre");
+    if (y && (!rstd_y || !dy || !dw_post)) return fail(DG_ERR_INVALID_ARG, "y needs rstd_y, dy and dw_post");
+    if (!y && (dy || dw_post)) return fail(DG_ERR_INVALID_ARG, "dy and dw_post come only with y");
+    if ((gate != nullptr) != (dgate != nullptr)) return fail(DG_ERR_INVALID_ARG, "dgate is required with gate, and only then");
+    if (dx_out && (rc = check_norm_rows("dx_out", dx_out, ld_dx_out, act_dtype, d)) != DG_OK) return rc;
+    if (dh && (rc = check_norm_rows("dh", dh, ld_dh, act_dtype, d)) != DG_OK) return rc;
+    if (w_pre && (rc = check_norm_rows("x", x, ld_x, act_dtype, d)) != DG_OK) return rc;
+    if (y && (rc = check_norm_rows("y", y, ld_y, act_dtype, d)) != DG_OK) return rc;
+    if (!aligned16(w_post) || !aligned16(gate) || !aligned16(w_pre) || !aligned16(dx) || !aligned16(dy) ||
+        !aligned16(dw_post) || !aligned16(dgate) || !aligned16(dw_pre))
+        return fail(DG_ERR_ALIGNMENT, "parameters and gradients must be 16-byte aligned");
+    const void* in[4] = {dx_out, dh, w_pre ? x : nullptr, y};
+    for (const void* q : in)
+        if (q && (q == dx || q == dy)) return fail(DG_ERR_INVALID_ARG, "dx and dy may not alias an input");
+    if (dx == dy) return fail(DG_ERR_INVALID_ARG, "dx and dy may not alias");
+    const size_t need = dg_block_norm_backward_workspace_size(B, C, d, gate != nullptr);
+    if (!workspace || workspace_bytes < need)
+        return fail(DG_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, need);
+    if (!aligned16(workspace)) return fail(DG_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+    if ((rc = check_device()) != DG_OK) return rc;
+    BlockNormBackwardParams p;
+    std::memset(&p, 0, sizeof(p));
+    const NormRuns n = norm_runs(B, C, gate != nullptr);
+    p.dx_out = dx_out;
+    p.dh = dh;
+    p.x = x;
+    p.y = y;
+    p.ld_dx_out = ld_dx_out;
+    p.ld_dh = ld_dh;
+    p.ld_x = ld_x;
+    p.ld_y = ld_y;
+    p.w_post = w_post;
+    p.gate = gate;
+    p.w_pre = w_pre;
+    p.rstd_y = rstd_y;
+    p.rstd_x = rstd_x;
+    p.B = n.B;
+    p.C = n.C;
+    p.d = d;
+    p.runs = n.runs;
+    p.run_rows = n.run_rows;
+    p.res_scale = res_scale;
+    p.dx = dx;
+    p.dy = dy;
+    p.dw_post = dw_post;
+    p.dgate = dgate;
+    p.dw_pre = dw_pre;
+    p.part_pre = static_cast<float*>(workspace);
+    p.part_post = p.part_pre + static_cast<size_t>(n.B) * n.runs * d;
+    const cudaError_t e = launch_block_norm_backward(p, act_dtype == DG_BF16, param_dtype == DG_BF16, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "block norm backward launch");
+    return DG_OK;
+}
+
+size_t dg_mx4_scale_bytes(int32_t rows, int32_t K) { return rows < 1 || K < 1 ? 0 : mx4_scale_bytes(rows, K); }
+
+int dg_mx4_quantize(const void* x, int dtype, int64_t ld, int32_t rows, int32_t K, uint8_t* codes, uint8_t* scales,
+                    dg_stream_t stream) {
+    g_last_error.clear();
+    int rc;
+    if (!x || !codes || !scales) return fail(DG_ERR_INVALID_ARG, "x, codes and scales are required");
+    if (!valid_dtype(dtype)) return fail(DG_ERR_INVALID_ARG, "dtype %d is not DG_F32 or DG_BF16", dtype);
+    if ((rc = check_mx4_matrix(rows, K)) != DG_OK) return rc;
+    if (ld < K) return fail(DG_ERR_INVALID_ARG, "ld = %lld is smaller than K = %d", (long long)ld, K);
+    if (!aligned16(x) || (ld * elt_size(dtype)) % 16 != 0 || !aligned16(codes) || !aligned16(scales))
+        return fail(DG_ERR_ALIGNMENT, "x (base and row stride), codes and scales must be 16-byte aligned");
+    if ((rc = check_device()) != DG_OK) return rc;
+    const cudaError_t e = launch_mx4_quantize(x, ld, dtype == DG_BF16, rows, K, codes, scales, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit quantisation launch");
+    return DG_OK;
+}
+
+int dg_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t K, void* out, int dtype,
+                      dg_stream_t stream) {
+    g_last_error.clear();
+    int rc;
+    if (!codes || !scales || !out) return fail(DG_ERR_INVALID_ARG, "codes, scales and out are required");
+    if (!valid_dtype(dtype)) return fail(DG_ERR_INVALID_ARG, "dtype %d is not DG_F32 or DG_BF16", dtype);
+    if ((rc = check_mx4_matrix(rows, K)) != DG_OK) return rc;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(out))
+        return fail(DG_ERR_ALIGNMENT, "codes, scales and out must be 16-byte aligned");
+    if ((rc = check_device()) != DG_OK) return rc;
+    const cudaError_t e = launch_mx4_dequantize(codes, scales, rows, K, out, dtype == DG_BF16, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit reading launch");
+    return DG_OK;
+}
+
+int dg_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales, int32_t M, int32_t N,
+                  int32_t K, void* out, int out_dtype, dg_stream_t stream) {
+    g_last_error.clear();
+    int rc;
+    if (!a || !a_scales || !w || !w_scales || !out)
+        return fail(DG_ERR_INVALID_ARG, "a, a_scales, w, w_scales and out are required");
+    if (!valid_dtype(out_dtype)) return fail(DG_ERR_INVALID_ARG, "out dtype %d is not DG_F32 or DG_BF16", out_dtype);
+    if ((rc = check_mx4_matrix(M, K)) != DG_OK) return rc;
+    if (N < 8 || N % 8 != 0) return fail(DG_ERR_INVALID_ARG, "N = %d must be a positive multiple of 8", N);
+    if (!aligned16(a) || !aligned16(a_scales) || !aligned16(w) || !aligned16(w_scales) || !aligned16(out))
+        return fail(DG_ERR_ALIGNMENT, "all operands must be 16-byte aligned");
+    if ((rc = check_device()) != DG_OK) return rc;
+    Mx4MatmulParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.a = a;
+    p.a_scales = a_scales;
+    p.w = w;
+    p.w_scales = w_scales;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.out_kind = out_dtype == DG_BF16 ? kMx4OutBf16 : kMx4OutF32;
+    p.out = out;
+    const cudaError_t e = launch_mx4_matmul(p, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");
+    return DG_OK;
+}
+
+size_t dg_ffw_mx4_workspace_size(int32_t rows, int32_t d, int32_t d_ff) {
+    if (rows < 1 || d < 64 || d_ff < 64) return 0;
+    return ffw_mx4_parts(rows, d, d_ff).total;
+}
+
+int dg_ffw_mx4(const void* z_in, int32_t rows, int32_t d, int32_t d_ff, const uint8_t* w1, const uint8_t* w1_scales,
+               const uint8_t* w2, const uint8_t* w2_scales, void* z_out, void* workspace, size_t workspace_bytes,
+               dg_stream_t stream) {
+    g_last_error.clear();
+    int rc;
+    if (!z_in || !w1 || !w1_scales || !w2 || !w2_scales || !z_out)
+        return fail(DG_ERR_INVALID_ARG, "z_in, w1, w1_scales, w2, w2_scales and z_out are required");
+    if (rows < 1) return fail(DG_ERR_INVALID_ARG, "rows = %d must be >= 1", rows);
+    if (d < 64 || d > 16384 || d % 64 != 0 || d_ff < 64 || d_ff > 16384 || d_ff % 64 != 0)
+        return fail(DG_ERR_INVALID_ARG, "d = %d and d_ff = %d must be multiples of 64 in [64, 16384]", d, d_ff);
+    if (!aligned16(z_in) || !aligned16(w1) || !aligned16(w1_scales) || !aligned16(w2) || !aligned16(w2_scales) || !aligned16(z_out))
+        return fail(DG_ERR_ALIGNMENT, "all operands must be 16-byte aligned");
+    const Mx4FfwParts n = ffw_mx4_parts(rows, d, d_ff);
+    if (!workspace || workspace_bytes < n.total)
+        return fail(DG_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, n.total);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(DG_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+    if ((rc = check_device()) != DG_OK) return rc;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    uint8_t *zq = ws, *zs = zq + n.z_codes, *hq = zs + n.z_scales, *hs = hq + n.h_codes;
+    cudaError_t e = launch_mx4_quantize(z_in, d, 1, rows, d, zq, zs, s);
+    if (e != cudaSuccess) return cuda_fail(e, "FFW input quantisation launch");
+    Mx4MatmulParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.a = zq;
+    p.a_scales = zs;
+    p.w = w1;
+    p.w_scales = w1_scales;
+    p.M = rows;
+    p.N = d_ff;
+    p.K = d;
+    p.out_kind = kMx4OutGelu;
+    p.out = hq;
+    p.out_scales = hs;
+    p.dependent = 1;
+    e = launch_mx4_matmul(p, s);
+    if (e != cudaSuccess) return cuda_fail(e, "FFW layer 1 launch");
+    p.a = hq;
+    p.a_scales = hs;
+    p.w = w2;
+    p.w_scales = w2_scales;
+    p.N = d;
+    p.K = d_ff;
+    p.out_kind = kMx4OutBf16;
+    p.out = z_out;
+    p.out_scales = nullptr;
+    e = launch_mx4_matmul(p, s);
+    if (e != cudaSuccess) return cuda_fail(e, "FFW layer 2 launch");
     return DG_OK;
 }
 

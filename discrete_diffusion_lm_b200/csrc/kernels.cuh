@@ -141,6 +141,56 @@ cudaError_t launch_ce_backward(const CeBackwardParams& p, cudaStream_t s);
 cudaError_t launch_selfcond_drop(uint16_t* z, int32_t n_seq, int64_t seq_elems, uint32_t key0, uint32_t key1,
                                  uint32_t step, uint8_t* keep, cudaStream_t s);
 
+// Norms around a block with gate and residual scale (block_norm.cu).  Null y: no norm after the
+// block (x is normalised as it is); null w_pre: no norm before the next block.
+struct BlockNormParams {
+    const void *x, *y;  // [R, d] with row strides ld_x, ld_y (elements)
+    int64_t ld_x, ld_y;
+    const void *w_post, *gate, *w_pre;  // [d], [R / C, d] or null, [d]
+    int32_t R, C, d;
+    float res_scale, eps;
+    void *x_out, *h;        // [R, d]
+    float *rstd_y, *rstd_x;  // [R] or null
+};
+cudaError_t launch_block_norm(const BlockNormParams& p, int act_bf16, int param_bf16, cudaStream_t s);
+
+struct BlockNormBackwardParams {
+    const void *dx_out, *dh, *x, *y;  // [R, d]; null dx_out: zero; null y or w_pre as above
+    int64_t ld_dx_out, ld_dh, ld_x, ld_y;
+    const void *w_post, *gate, *w_pre;
+    const float *rstd_y, *rstd_x;
+    int32_t B, C, d;           // without a gate: one canvas of all rows
+    int32_t runs, run_rows;    // runs of rows per canvas
+    float res_scale;
+    void *dx, *dy;             // [R, d]
+    float *dw_post, *dgate, *dw_pre;
+    float *part_pre, *part_post;  // [B * runs, d] partial sums
+};
+int32_t block_norm_runs(int32_t B, int32_t C);
+cudaError_t launch_block_norm_backward(const BlockNormBackwardParams& p, int act_bf16, int param_bf16, cudaStream_t s);
+
+// Microscaled 4-bit floating point (mx4.cu): scale tiles, quantisation, reading back, products.
+size_t mx4_scale_bytes(int32_t rows, int32_t K);
+cudaError_t launch_mx4_quantize(const void* x, int64_t ld, int is_bf16, int32_t rows, int32_t K, uint8_t* codes,
+                                uint8_t* scales, cudaStream_t s);
+cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t K, void* out,
+                                  int is_bf16, cudaStream_t s);
+enum Mx4OutKind : int {
+    kMx4OutBf16 = 0,
+    kMx4OutF32 = 1,
+    kMx4OutGelu = 2,  // gelu of the product, quantised again
+};
+struct Mx4MatmulParams {
+    const uint8_t *a, *a_scales, *w, *w_scales;
+    int32_t M, N, K;
+    int32_t out_kind;
+    void* out;            // [M, N] bf16 or fp32, or codes [M, N / 2]
+    uint8_t* out_scales;  // kMx4OutGelu
+    int32_t dependent;    // 1: launch as a programmatic dependent of the kernel that writes a
+};
+cudaError_t launch_mx4_matmul(const Mx4MatmulParams& p, cudaStream_t s);
+cudaError_t read_and_clear_mx4_error(int* out);
+
 // The sampler step behind the two C entry points (dg_sampler_step, dg_sampler_step_noalloc): all
 // arguments are checked first; with clear_ws the workspace is then zeroed on the stream before the
 // launches.  Returns a DG_* status.

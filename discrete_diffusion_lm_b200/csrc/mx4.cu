@@ -1,0 +1,493 @@
+// Microscaled 4-bit floating point (OCP Microscaling Formats, MXFP4): quantisation, reading back, and
+// products on the sm_100a tensor cores.
+//
+// Thirty-two consecutive values of a row share the scale 2^(c - 127), kept as the byte c (E8M0); a
+// value is E2M1: 0, 0.5, 1, 1.5, 2, 3, 4 or 6 with a sign, two to a byte, the lower index in the low
+// half.  For a block of largest magnitude A,
+//   e = max(floor(log2 A) - 2, -127), c = e + 127, q_i = round-to-nearest-even(x_i 2^-e), |q_i| <= 6
+// (6 = 1.5 2^2 is the largest E2M1 value, so e puts A between 4 and 8); A = 0 gives c = 0; a block
+// with a NaN or an infinity gets c = 255, which stands for NaN.
+// Scale bytes lie as the tensor core takes them: tiles of 128 rows x 4 blocks (128 values), 512
+// bytes, byte (r % 32) * 16 + (r / 32 % 4) * 4 + block % 4; tiles of one row group are consecutive.
+// Padding in a tile (rows or blocks past the matrix) holds 127.
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include "common.cuh"
+#include "kernels.cuh"
+#include "tensor_core.cuh"
+
+namespace dg {
+
+namespace {
+
+constexpr uint32_t kUnitScale = 127;  // the scale byte of 2^0
+
+// The scale byte of a block whose largest magnitude has the bit pattern `top` (sign cleared).
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+    if (top >= 0x7F800000u) return 255u;
+    const uint32_t ex = top >> 23;  // biased exponent; 0 for zero and subnormal values, whose e is -127
+    return ex > 2u ? ex - 2u : 0u;
+}
+// 2^-e as a float for a scale byte c = e + 127 in [0, 252]: exponents 127 down to -125, all normal.
+__device__ __forceinline__ float inverse_scale(uint32_t c) { return __uint_as_float((254u - c) << 23); }
+
+// Eight values times `inv`, rounded to E2M1 (nearest, ties to even, saturating), packed low to high.
+__device__ __forceinline__ uint32_t pack_e2m1(const float (&f)[8], float inv) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(f[0] * inv), "f"(f[1] * inv), "f"(f[2] * inv), "f"(f[3] * inv), "f"(f[4] * inv), "f"(f[5] * inv),
+          "f"(f[6] * inv), "f"(f[7] * inv));
+    return r;
+}
+
+// ------------------------------------------------------------------------------------ quantisation
+// Four lanes per block, eight values per lane; a warp takes eight consecutive blocks of a row per
+// step (256 values), so loads, code stores (4 bytes per lane) and the two scale words are
+// contiguous.  Rows up to a multiple of 128 are walked so that every scale tile is written whole.
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+    const uint4 a = ld_stream_v4(p), b = ld_stream_v4(p + 4);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
+    const uint4 a = ld_stream_v4(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(w[i]);
+        f[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_quantize_kernel(const T* __restrict__ x, int64_t ld, int32_t rows, int32_t K,
+                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+    const int32_t k_tiles = (K + 127) / 128;
+    const int32_t steps = (k_tiles + 1) / 2;  // 256 values per warp and step
+    const int64_t padded = (static_cast<int64_t>(rows) + 127) / 128 * 128;
+    const int lane = threadIdx.x & 31;
+    const int64_t n = padded * steps, stride = static_cast<int64_t>(gridDim.x) * 8;
+    grid_launch_dependents();
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < n; u += stride) {
+        const int64_t r = u / steps;
+        const int32_t k = static_cast<int32_t>(u - r * steps) * 256 + lane * 8;
+        uint32_t c = kUnitScale;
+        if (r < rows) {  // the whole warp
+            const bool in = k < K;  // K is a multiple of 32: the four lanes of a block agree
+            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (in) load8(x + r * ld + k, f);
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            if (in) {
+                c = scale_byte(top);
+                const uint32_t q = c == 255u ? 0u : pack_e2m1(f, inverse_scale(c));
+                *reinterpret_cast<uint32_t*>(codes + r * (K / 2) + k / 2) = q;
+            }
+        }
+        // the scale bytes of four blocks (16 lanes) as one word of their tile
+        uint32_t word = c << (8 * (lane >> 2 & 3));
+        word |= __shfl_xor_sync(0xffffffffu, word, 4);
+        word |= __shfl_xor_sync(0xffffffffu, word, 8);
+        const int32_t kt = k / 128;
+        if ((lane & 15) == 0 && kt < k_tiles)
+            *reinterpret_cast<uint32_t*>(scales + ((r / 128) * k_tiles + kt) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4) = word;
+    }
+}
+
+// ------------------------------------------------------------------------------------ reading back
+__device__ __forceinline__ float e2m1_value(uint32_t q) {
+    const uint32_t e = q >> 1 & 3u, m = q & 1u;
+    // exponent 0 is the subnormal 0.5 m; else (1 + m / 2) 2^(e - 1)
+    const float v = e ? __uint_as_float((126u + e) << 23 | m << 22) : 0.5f * static_cast<float>(m);
+    return q & 8u ? -v : v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                             int32_t rows, int32_t K, T* __restrict__ out) {
+    const int32_t k_tiles = (K + 127) / 128, per_row = K / 8;
+    const int64_t n = static_cast<int64_t>(rows) * per_row;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u < n; u += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = u / per_row;
+        const int32_t k = static_cast<int32_t>(u - r * per_row) * 8;
+        const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(codes + u * 4));
+        const uint32_t c = __ldg(scales + ((r / 128) * k_tiles + k / 128) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4 + (k / 32 & 3));
+        // 2^(c - 127): c = 0 is the subnormal 2^-127, 255 is NaN
+        const float s = c == 255u ? __uint_as_float(0x7FC00000u) : c ? __uint_as_float(c << 23) : __uint_as_float(0x00400000u);
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = e2m1_value(q >> (4 * i) & 15u) * s;
+        T* o = out + u * 8;
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                      pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+        } else {
+            *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<float4*>(o + 4) = make_float4(f[4], f[5], f[6], f[7]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------ product
+// out[M, N] = A[M, K] W[N, K]^T, both operands MXFP4 with K-contiguous rows, fp32 accumulation.
+//
+// A CTA computes 128 rows x 128 columns over a run of 256-value blocks of K.  Per block, one thread
+// copies the W tile (128-byte rows, 128-byte swizzle) and its scale tiles, another the A tile and
+// its scale tiles (it waits for the preceding kernel first: A may be that kernel's output); the
+// MMA thread moves the scales into tensor memory (tcgen05.cp) and issues four
+// tcgen05.mma.kind::mxf4 of K = 64, two scale bytes per row and instruction.
+// With few tiles K is split over the CTAs of a cluster: each leaves its fp32 tile in shared memory
+// and the CTAs add the tiles, each a share of the rows, in a fixed order.
+constexpr int kMTile = 128, kNTile = 128, kKStage = 256;
+constexpr int kMx4Threads = 192;  // W producer, MMA issuer, four epilogue warps (the first also copies A)
+constexpr uint32_t kOperandBytes = 128 * kKStage / 2;
+constexpr uint32_t kScaleBytes = 1024;  // two tiles
+constexpr uint32_t kStageBytes = 2 * (kOperandBytes + kScaleBytes);
+constexpr int kMx4Stages = 6;
+constexpr uint32_t kTmemCols = 256;  // 128 accumulator columns, 16 per stage of scales
+constexpr int kTilePitch = kNTile + 4;  // floats; rows 16 bytes off the banks of the row before
+constexpr uint32_t kMx4Smem = kMx4Stages * kStageBytes + 256 + 1024;
+static_assert(kMx4Stages * 16 + kNTile <= static_cast<int>(kTmemCols), "scales and accumulator fit");
+static_assert(kMTile * kTilePitch * 4 <= kMx4Stages * kStageBytes, "the fp32 tile fits the drained ring");
+
+enum Mx4Out : int { kOutBf16 = 0, kOutF32 = 1, kOutGeluMx4 = 2 };
+
+struct alignas(64) Mx4Kernel {
+    CUtensorMap tm_a, tm_w;  // bytes [rows, K / 2], box 128 rows x 128 bytes
+    const uint8_t *sa, *sw;
+    void* out;            // bf16 or fp32 [M, N], or codes [M, N / 2]
+    uint8_t* out_scales;  // kOutGeluMx4
+    int32_t M, N, K;
+    int32_t n_tiles, k_tiles, k_blocks;  // 128-column tiles; 128-value and 256-value steps of K
+    long long wait_limit;
+};
+
+// kind::mxf4 instruction descriptor: E2M1 operands (type 1), E8M0 scales, M = 128, N = 128; the scale
+// bytes of operand A at bit 29, of B at bit 4 (which two of a word's four).
+__device__ __forceinline__ uint32_t idesc_mx4(uint32_t pair) {
+    return (pair << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kNTile >> 3) << 17) | (1u << 23) |
+           (static_cast<uint32_t>(kMTile >> 7) << 27) | (pair << 29);
+}
+__device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+// 32 rows x 16 bytes of shared memory to four tensor-memory columns, repeated for the four lane groups.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem_addr) {
+    const uint64_t d = smem_desc(smem_addr, 16, 128, 0);  // no swizzle, groups of 8 rows 128 bytes apart
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+}
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+    return r;
+}
+
+// GELU, tanh form, as x / (1 + exp(-2u)): the hidden layer is rounded to 4 bits by comparisons with
+// the E2M1 midpoints, so an error here moves values across them; the hardware tanh's 2^-11 would
+// move one value in a few hundred, ex2 and a division (about 2^-22) one in a million.
+__device__ __forceinline__ float gelu_exact(float x) {
+    const float k = -2.0f * 0.7978845608028654f * kLog2e;  // -2 sqrt(2 / pi) log2 e
+    const float u = k * fmaf(0.044715f * x, x * x, x);
+    return __fdividef(x, 1.0f + exp2f(fminf(u, 126.0f)));
+}
+
+template <int kOut>
+__global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid_constant__ Mx4Kernel p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kMx4Stages * kStageBytes);
+    uint64_t* empty = full + kMx4Stages;
+    uint64_t* accum = empty + kMx4Stages;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accum + 1);
+    WaitCtl* wc = reinterpret_cast<WaitCtl*>(tmem_slot + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t splits = cluster_size(), split = cluster_rank();
+    const int32_t tile = blockIdx.x / splits;
+    const int32_t mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
+    const int32_t kb0 = static_cast<int32_t>(static_cast<int64_t>(p.k_blocks) * split / splits);
+    const int32_t kb1 = static_cast<int32_t>(static_cast<int64_t>(p.k_blocks) * (split + 1) / splits);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kMx4Stages; ++s) {
+            mbar_init(&full[s], 2);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(accum, 1);
+        wc->abort = 0;
+        wc->limit = p.wait_limit;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    if ((warp == 0 || warp == 2) && lane == 0) {
+        // ---------------------------------------------------------------- producers: W, A
+        const bool is_a = warp == 2;
+        const CUtensorMap* tm = is_a ? &p.tm_a : &p.tm_w;
+        const int32_t rt = is_a ? mt : nt;
+        const uint8_t* scales = (is_a ? p.sa : p.sw) + static_cast<int64_t>(rt) * p.k_tiles * 512;
+        const uint32_t offset = is_a ? 0 : kOperandBytes;
+        const uint32_t scale_offset = 2 * kOperandBytes + (is_a ? 0 : kScaleBytes);
+        if (is_a) grid_dependency_wait();
+        int32_t kb = kb0;
+        for (; kb < kb1; ++kb) {
+            const int i = kb - kb0, s = i % kMx4Stages;
+            if (!mbar_wait(&empty[s], ((i / kMx4Stages) & 1) ^ 1, wc)) break;
+            uint8_t* st = smem + s * kStageBytes;
+            const uint32_t scale_bytes = min(2, p.k_tiles - 2 * kb) * 512;
+            mbar_arrive_expect_tx(&full[s], kOperandBytes + scale_bytes);
+            tma_load_2d(st + offset, tm, kb * (kKStage / 2), rt * 128, &full[s]);
+            bulk_load(st + scale_offset, scales + static_cast<int64_t>(kb) * 1024, scale_bytes, &full[s]);
+        }
+        if (aborted(wc)) {  // let the copies in flight land before the shared memory goes away
+            const long long t0 = clock64();
+            for (int i = max(0, kb - kb0 - kMx4Stages); i < kb - kb0; ++i)
+                while (!mbar_try_wait(&full[i % kMx4Stages], (i / kMx4Stages) & 1) && clock64() - t0 < wc->limit) {
+                }
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ---------------------------------------------------------------- MMA issuer
+        for (int32_t kb = kb0; kb < kb1; ++kb) {
+            const int i = kb - kb0, s = i % kMx4Stages;
+            if (!mbar_wait(&full[s], (i / kMx4Stages) & 1, wc)) break;
+            tcgen05_after_sync();
+            const uint32_t st = smem_u32(smem + s * kStageBytes);
+            const uint32_t sf = tmem + kNTile + s * 16;  // two tiles of A, two of W, four columns each
+            const int32_t tiles = min(2, p.k_tiles - 2 * kb);
+            for (int j = 0; j < tiles; ++j) {
+                copy_scales(sf + 4 * j, st + 2 * kOperandBytes + 512 * j);
+                copy_scales(sf + 8 + 4 * j, st + 2 * kOperandBytes + kScaleBytes + 512 * j);
+            }
+            const int32_t steps = min(4, (p.K - kb * kKStage + 63) / 64);
+            for (int ks = 0; ks < steps; ++ks)
+                umma_mx4(tmem, smem_desc(st + ks * 32, 16, 1024, kLayoutSw128),
+                         smem_desc(st + kOperandBytes + ks * 32, 16, 1024, kLayoutSw128), idesc_mx4((ks & 1) * 2),
+                         sf + 4 * (ks >> 1), sf + 8 + 4 * (ks >> 1), (i > 0 || ks > 0) ? 1u : 0u);
+            umma_commit(&empty[s]);
+        }
+        umma_commit(accum);
+    }
+    __syncwarp();
+
+    // ---------------------------------------------------------------- epilogue: fp32 tile, then rows
+    const int32_t m_valid = min(kMTile, p.M - mt * kMTile);
+    float* tile_f = reinterpret_cast<float*>(smem);
+    bool ok = true;
+    if (warp >= 2) {
+        ok = __all_sync(0xffffffffu, mbar_wait(accum, 0, wc));
+        const int quarter = warp & 3;
+        if (ok && quarter * 32 < m_valid) {
+            tcgen05_after_sync();
+            const int row = quarter * 32 + lane;
+#pragma unroll
+            for (int c = 0; c < kNTile; c += 32) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, v);
+                if (row < m_valid) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        st_shared_v4(smem_u32(tile_f + row * kTilePitch + c + 4 * q), make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
+                }
+            }
+        }
+    }
+    grid_launch_dependents();
+    ok = __syncthreads_and(ok);
+    if (splits > 1) cluster_sync();  // every split's tile is in place
+    const int32_t n0 = nt * kNTile;
+    const int32_t col = n0 + lane * 4;
+    // rows split, split + splits, ... of the tile, over the CTA's six warps; a lane takes four columns
+    const int32_t last = kOut == kOutGeluMx4 ? kMTile : m_valid;  // whole scale tiles
+    for (int32_t i = split + splits * warp; ok && i < last; i += splits * (kMx4Threads / 32)) {
+        const int64_t r = static_cast<int64_t>(mt) * kMTile + i;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < m_valid) {
+            const uint32_t at = smem_u32(tile_f + i * kTilePitch + lane * 4);
+            if (splits == 1) {
+                v = *reinterpret_cast<const float4*>(tile_f + i * kTilePitch + lane * 4);
+            } else {
+                float4 w[8];
+#pragma unroll
+                for (uint32_t s = 0; s < 8; ++s)
+                    if (s < splits) w[s] = ld_cluster_f4(map_to_rank(at, s));
+                v = w[0];
+#pragma unroll
+                for (uint32_t s = 1; s < 8; ++s)
+                    if (s < splits) {
+                        v.x += w[s].x;
+                        v.y += w[s].y;
+                        v.z += w[s].z;
+                        v.w += w[s].w;
+                    }
+            }
+        }
+        if (kOut == kOutF32) {
+            if (col < p.N) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + r * p.N + col) = v;
+        } else if (kOut == kOutBf16) {
+            if (col < p.N)
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + r * p.N + col) =
+                    make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        } else {
+            // eight lanes hold a block of 32 hidden values
+            const float f[4] = {gelu_exact(v.x), gelu_exact(v.y), gelu_exact(v.z), gelu_exact(v.w)};
+            uint32_t top = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) top = max(top, __float_as_uint(f[q]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const bool in = i < m_valid && col < p.N;
+            const uint32_t c = in ? scale_byte(top) : kUnitScale;
+            if (in) {
+                const float g[8] = {f[0], f[1], f[2], f[3], 0.f, 0.f, 0.f, 0.f};
+                const uint32_t q = c == 255u ? 0u : pack_e2m1(g, inverse_scale(c));
+                *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.out) + r * (p.N / 2) + col / 2) = static_cast<uint16_t>(q);
+            }
+            uint32_t word = c << (8 * (lane >> 3));
+            word |= __shfl_xor_sync(0xffffffffu, word, 8);
+            word |= __shfl_xor_sync(0xffffffffu, word, 16);
+            if (lane == 0)
+                *reinterpret_cast<uint32_t*>(p.out_scales + (static_cast<int64_t>(mt) * p.n_tiles + nt) * 512 + (i % 32) * 16 + (i / 32) * 4) = word;
+        }
+    }
+    if (splits > 1) cluster_sync();  // no CTA leaves while another reads its tile
+    tcgen05_before_sync();
+    __syncthreads();
+    tcgen05_after_sync();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+template <int kOut>
+cudaError_t launch_product(const Mx4Kernel& kp, int grid, int splits, bool dependent, cudaStream_t st) {
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [] {
+        attr_err = cudaFuncSetAttribute(mx4_matmul_kernel<kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMx4Smem));
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kMx4Threads);
+    cfg.dynamicSmemBytes = kMx4Smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, mx4_matmul_kernel<kOut>, kp);
+    if (e != cudaSuccess) return e;
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t mx4_scale_bytes(int32_t rows, int32_t K) {
+    return static_cast<size_t>((static_cast<int64_t>(rows) + 127) / 128) * ((static_cast<int64_t>(K) + 127) / 128) * 512;
+}
+
+cudaError_t launch_mx4_quantize(const void* x, int64_t ld, int is_bf16, int32_t rows, int32_t K, uint8_t* codes, uint8_t* scales,
+                                cudaStream_t st) {
+    const int64_t warps = (static_cast<int64_t>(rows) + 127) / 128 * 128 * (((K + 127) / 128 + 1) / 2);
+    const int blocks = static_cast<int>(std::min<int64_t>((warps + 7) / 8, 8LL * num_sms()));
+    if (is_bf16)
+        mx4_quantize_kernel<<<blocks, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x), ld, rows, K, codes, scales);
+    else
+        mx4_quantize_kernel<<<blocks, 256, 0, st>>>(static_cast<const float*>(x), ld, rows, K, codes, scales);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t K, void* out, int is_bf16,
+                                  cudaStream_t st) {
+    const int64_t n = static_cast<int64_t>(rows) * (K / 8);
+    const int blocks = static_cast<int>(std::min<int64_t>((n + 255) / 256, 16LL * num_sms()));
+    if (is_bf16)
+        mx4_dequantize_kernel<<<blocks, 256, 0, st>>>(codes, scales, rows, K, static_cast<__nv_bfloat16*>(out));
+    else
+        mx4_dequantize_kernel<<<blocks, 256, 0, st>>>(codes, scales, rows, K, static_cast<float*>(out));
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
+    Mx4Kernel kp;
+    std::memset(&kp, 0, sizeof(kp));
+    cudaError_t e = encode_2d(&kp.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.a, q.K / 2, q.M, q.K / 2, 128, kMTile, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess)
+        e = encode_2d(&kp.tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.w, q.K / 2, q.N, q.K / 2, 128, kNTile, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    kp.sa = q.a_scales;
+    kp.sw = q.w_scales;
+    kp.out = q.out;
+    kp.out_scales = q.out_scales;
+    kp.M = q.M;
+    kp.N = q.N;
+    kp.K = q.K;
+    kp.n_tiles = (q.N + kNTile - 1) / kNTile;
+    kp.k_tiles = (q.K + 127) / 128;
+    kp.k_blocks = (q.K + kKStage - 1) / kKStage;
+    kp.wait_limit = kWaitLimitCycles;
+    const int64_t tiles = static_cast<int64_t>((q.M + kMTile - 1) / kMTile) * kp.n_tiles;
+    // split K while the clusters fit one wave and every split keeps a block
+    int splits = 1;
+    while (splits < 8 && 2 * splits * tiles <= num_sms() && 2 * splits <= kp.k_blocks) splits *= 2;
+    const int64_t grid = tiles * splits;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (q.out_kind == kMx4OutF32) return launch_product<kOutF32>(kp, static_cast<int>(grid), splits, q.dependent != 0, st);
+    if (q.out_kind == kMx4OutBf16) return launch_product<kOutBf16>(kp, static_cast<int>(grid), splits, q.dependent != 0, st);
+    return launch_product<kOutGeluMx4>(kp, static_cast<int>(grid), splits, q.dependent != 0, st);
+}
+
+cudaError_t read_and_clear_mx4_error(int* out) {
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int));
+    if (e != cudaSuccess) return e;
+    if (v) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
+    }
+    *out = v;
+    return e;
+}
+
+}  // namespace dg

@@ -322,6 +322,118 @@ int dg_ffw(const void* z_in, int32_t rows, int32_t d, int32_t d_ff, const void* 
            void* hidden, void* z_out, void* workspace, size_t workspace_bytes, dg_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Norms around a block with its gate and residual scale.  The pages name no */
+/* norm; this is the form that a pre- and post-normed transformer block has */
+/* around dg_ffw, where the self-conditioning state joins the decoder's     */
+/* input.  Per row r = b*C + i over d columns, n(v) = v rsqrt(mean v^2 + eps):*/
+/*   x_out[r] = x[r] + res_scale gate[b] w_post n(y[r])   (after a block)   */
+/*   h[r]     = w_pre n(x_out[r])                  (before the next block)  */
+/* y == NULL: no norm after a block, h is taken of x itself (x_out, w_post  */
+/* and gate NULL too).  w_pre == NULL: no norm before the next (h NULL too).*/
+/* gate == NULL: 1.  Sums and statistics are fp32; h is taken of x_out as it */
+/* is before it is rounded to act_dtype.                                     */
+/* x, y: device act_dtype [B*C, d] with row strides ld_x, ld_y >= d         */
+/* (elements; base and stride multiples of 16 bytes).  w_post, w_pre:       */
+/* device param_dtype [d]; gate: device param_dtype [B, d].                 */
+/* x_out, h: device act_dtype [B*C, d], contiguous.  x_out may be x itself  */
+/* where ld_x = d; otherwise no output aliases an input or another output.  */
+/* rstd_y, rstd_x: device float [B*C], the reciprocal root means that the   */
+/* backward pass takes, or NULL.                                             */
+/* d is a multiple of 8 in [8, 16384]; 1 <= B <= DG_MAX_CANVASES, C >= 1,   */
+/* B*C < 2^31; eps >= 0.  One launch, no workspace.                         */
+/* ------------------------------------------------------------------------ */
+int dg_block_norm(const void* x, int64_t ld_x, const void* y, int64_t ld_y, int act_dtype,
+                  const void* w_post, const void* gate, const void* w_pre, int param_dtype,
+                  int32_t B, int32_t C, int32_t d, float res_scale, float eps, void* x_out, void* h,
+                  float* rstd_y, float* rstd_x, dg_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Gradients of dg_block_norm.  dx_out: gradient of the stream x_out (NULL: */
+/* zero); dh: gradient of h; x: the stream that h was taken of (the forward */
+/* call's x_out, or its x where it had no y); y, the parameters and the     */
+/* rstd vectors as the forward call had and wrote them.  With v = y rstd_y, */
+/* m = x rstd_x, t = dh w_pre, c = res_scale gate w_post:                    */
+/*   dx = dx_out + rstd_x (t - m mean(t m)),  dy = rstd_y (c dx - v mean(c dx v))*/
+/*   dw_pre = sum_r dh m,  P_b = sum_{r in b} dx v,                          */
+/*   dw_post = res_scale sum_b gate_b P_b,  dgate_b = res_scale w_post P_b.  */
+/* (dx in dy and P is the unrounded one.)  dx is the gradient of the forward */
+/* call's x.  Without w_pre: dh, x, rstd_x and dw_pre are NULL; without y:  */
+/* y, rstd_y, dy and dw_post; dgate goes with gate.                          */
+/* dx_out, dh, x, y: device act_dtype [B*C, d] with row strides as above;   */
+/* dx, dy: device act_dtype [B*C, d], contiguous, aliasing nothing;         */
+/* dw_post, dw_pre: device float [d], dgate: device float [B, d].           */
+/* The sums over rows have a fixed order: results repeat bit for bit.       */
+/* Workspace: dg_block_norm_backward_workspace_size bytes, 16-byte aligned, */
+/* any contents.  Two launches.                                              */
+/* ------------------------------------------------------------------------ */
+size_t dg_block_norm_backward_workspace_size(int32_t B, int32_t C, int32_t d, int have_gate);
+
+int dg_block_norm_backward(const void* dx_out, int64_t ld_dx_out, const void* dh, int64_t ld_dh,
+                           const void* x, int64_t ld_x, const void* y, int64_t ld_y, int act_dtype,
+                           const void* w_post, const void* gate, const void* w_pre, int param_dtype,
+                           int32_t B, int32_t C, int32_t d, float res_scale, const float* rstd_y,
+                           const float* rstd_x, void* dx, void* dy, float* dw_post, float* dgate,
+                           float* dw_pre, void* workspace, size_t workspace_bytes,
+                           dg_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Microscaled 4-bit floating point (OCP Microscaling Formats 1.0, MXFP4).   */
+/* A matrix [rows, K], K a multiple of 32, is held as                        */
+/*   codes  uint8 [rows, K/2]: two E2M1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6,  */
+/*          and a sign bit) to a byte, the lower column in the low half;    */
+/*   scales uint8 [ceil(rows/128), ceil(K/128), 32, 16]: one E8M0 byte c    */
+/*          (2^(c-127); 255 = NaN) per row and 32 columns, in tiles of 128   */
+/*          rows x 4 blocks as the tensor cores read them: row r, block q at */
+/*          [r/128, q/4, r%32, (r/32%4)*4 + q%4].  dg_mx4_scale_bytes bytes. */
+/*          Padding (rows past the matrix, blocks past K) holds 127;         */
+/*          dg_mx4_matmul needs it in the blocks past K: a 255 there would   */
+/*          make NaNs.                                                       */
+/* dg_mx4_quantize: for a block of largest magnitude A, e = max(floor(log2 A)*/
+/*   - 2, -127), c = e + 127 (A = 0: c = 0); every value x goes to the       */
+/*   nearest of the eight magnitudes to |x| 2^-e (ties to the even code, past*/
+/*   6 to 6).  A block with a NaN or an infinity gets c = 255.  x: device    */
+/*   DG_F32 or DG_BF16 [rows, K], row stride ld >= K, base and stride        */
+/*   multiples of 16 bytes.  Writes codes and every byte of scales.          */
+/* dg_mx4_dequantize: the values, as DG_F32 (exact; subnormal results are    */
+/*   kept) or DG_BF16 (exact except where 2^(c-127) leaves its range) in out */
+/*   [rows, K], contiguous.                                                  */
+/* All pointers 16-byte aligned, nothing aliased, no workspace, one launch.  */
+/* ------------------------------------------------------------------------ */
+size_t dg_mx4_scale_bytes(int32_t rows, int32_t K);
+
+int dg_mx4_quantize(const void* x, int dtype, int64_t ld, int32_t rows, int32_t K, uint8_t* codes,
+                    uint8_t* scales, dg_stream_t stream);
+
+int dg_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t K,
+                      void* out, int dtype, dg_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Product of two MXFP4 matrices on the tensor cores, out = A W^T with fp32  */
+/* accumulation: a, a_scales [M, K], w, w_scales [N, K] as above; out: device*/
+/* DG_F32 or DG_BF16 [M, N], contiguous, 16-byte aligned, aliasing nothing.  */
+/* N is a multiple of 8, K of 32, M >= 1.  A scale of 255 makes its row (of A)*/
+/* or column (of W) NaN.  One launch, no workspace.                          */
+/* ------------------------------------------------------------------------ */
+int dg_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w,
+                  const uint8_t* w_scales, int32_t M, int32_t N, int32_t K, void* out, int out_dtype,
+                  dg_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The feed-forward block of dg_ffw in MXFP4: z_in is quantised, then        */
+/*   hidden = gelu(z_in W1), quantised from fp32, and z_out = hidden W2,     */
+/* gelu in its tanh form.  z_in, z_out: device bf16 [rows, d]; w1, w1_scales:*/
+/* W1 transposed, [d_ff, d] as dg_mx4_quantize writes it; w2, w2_scales: W2  */
+/* transposed, [d, d_ff].  z_out may be z_in.  d, d_ff multiples of 64 in    */
+/* [64, 16384].  Workspace: dg_ffw_mx4_workspace_size bytes, 256-byte        */
+/* aligned, any contents.  Three launches.                                   */
+/* ------------------------------------------------------------------------ */
+size_t dg_ffw_mx4_workspace_size(int32_t rows, int32_t d, int32_t d_ff);
+
+int dg_ffw_mx4(const void* z_in, int32_t rows, int32_t d, int32_t d_ff, const uint8_t* w1,
+               const uint8_t* w1_scales, const uint8_t* w2, const uint8_t* w2_scales, void* z_out,
+               void* workspace, size_t workspace_bytes, dg_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Allocation-free sampler step.  The pages have no counterpart: this entry  */
 /* point exists for callers that cannot allocate device memory where they   */
 /* sample (a serving loop that must not call cudaMalloc, which can stall the */
