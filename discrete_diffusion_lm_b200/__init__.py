@@ -606,33 +606,41 @@ def _dtype_of(t: torch.Tensor, name: str) -> int:
 
 def _arg(t: torch.Tensor, name: str, dev: int, dtype, shape) -> int:
     """Device address of a contiguous tensor argument of the given dtype and shape on device `dev`."""
-    if t.get_device() != dev:
-        _wrong_device(t, name)
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dev, dtype, shape)
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows_arg(t: torch.Tensor, name: str, dev: int, dtype, shape):
     """Device address and row stride of a 2-D tensor whose last dimension is contiguous."""
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev):
+        _refuse(t, name, dev, dtype, shape)
+    s0, s1 = t.stride()
+    if s1 != 1:
+        raise ValueError(f"{name} must have unit stride along the last dim")
+    return t.data_ptr(), (s0 if shape[0] > 1 else shape[1])
+
+
+def _refuse(t: torch.Tensor, name: str, dev: int, dtype, shape):
     if t.get_device() != dev:
         _wrong_device(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be of shape {list(shape)}, got {list(t.shape)}")
-    s0, s1 = t.stride()
-    if s1 != 1 and shape[1] != 1:
-        raise ValueError(f"{name} must have unit stride along the last dim")
-    return t.data_ptr(), (s0 if shape[0] > 1 else shape[1])
 
 
 def _wrong_device(t: torch.Tensor, name: str):
     if not t.is_cuda:
         raise ValueError("the library takes CUDA tensors only (got %s on %s)" % (name, t.device))
     raise ValueError(f"{name} is on {t.device}, another device than the first argument")
+
+
+# The current stream's handle on a device: without the Stream object that torch.cuda.current_stream builds
+# (3 us of a call that costs the GPU as little).
+_current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _device_of(t: torch.Tensor, name: str) -> int:
@@ -655,10 +663,6 @@ class _On:
     def __exit__(self, *exc):
         for p in reversed(self.parts):
             p.__exit__(*exc)
-
-
-def _given(out: Optional[dict], key: str):
-    return None if out is None else out.get(key)
 
 
 def dg_block_norm(x: torch.Tensor, w_pre: Optional[torch.Tensor] = None, *, y: Optional[torch.Tensor] = None,
@@ -685,7 +689,18 @@ def dg_block_norm(x: torch.Tensor, w_pre: Optional[torch.Tensor] = None, *, y: O
     if given is None:
         raise ValueError("w_pre or w_post (with y) is needed")
     ptype, par = given.dtype, _dtype_of(given, "w_pre" if w_pre is not None else "w_post")
-    res = {}
+    res, device = {}, x.device
+
+    def new(key, dt, shp):
+        t = None if out is None else out.get(key)
+        if t is not None:
+            p = _arg(t, key, dev, dt, shp)
+        else:
+            t = torch.empty_like(x, memory_format=torch.contiguous_format) if shp is shape else torch.empty(shp, dtype=dt, device=device)
+            p = t.data_ptr()
+        res[key] = t
+        return p
+
     py = pw = pg = pn = po = ph = pry = prx = None
     ld_y = d
     if y is not None:
@@ -695,18 +710,14 @@ def dg_block_norm(x: torch.Tensor, w_pre: Optional[torch.Tensor] = None, *, y: O
         pw = _arg(w_post, "w_post", dev, ptype, (d,))
         if gate is not None:
             pg = _arg(gate, "gate", dev, ptype, (R // C, d))
-        res["x"] = o = _given(out, "x") if _given(out, "x") is not None else torch.empty(shape, dtype=dtype, device=x.device)
-        res["rstd_y"] = ry = _given(out, "rstd_y") if _given(out, "rstd_y") is not None else torch.empty(R, dtype=torch.float32, device=x.device)
-        po, pry = _arg(o, 'out["x"]', dev, dtype, shape), _arg(ry, 'out["rstd_y"]', dev, torch.float32, (R,))
+        po, pry = new("x", dtype, shape), new("rstd_y", torch.float32, (R,))
     elif w_post is not None or gate is not None:
         raise ValueError("w_post and gate come only with y")
     if w_pre is not None:
         pn = _arg(w_pre, "w_pre", dev, ptype, (d,))
-        res["h"] = h = _given(out, "h") if _given(out, "h") is not None else torch.empty(shape, dtype=dtype, device=x.device)
-        res["rstd_x"] = rx = _given(out, "rstd_x") if _given(out, "rstd_x") is not None else torch.empty(R, dtype=torch.float32, device=x.device)
-        ph, prx = _arg(h, 'out["h"]', dev, dtype, shape), _arg(rx, 'out["rstd_x"]', dev, torch.float32, (R,))
+        ph, prx = new("h", dtype, shape), new("rstd_x", torch.float32, (R,))
     rc = lib().dg_block_norm(px, ld_x, py, ld_y, act, pw, pg, pn, par, R // C, C, d, res_scale, eps, po, ph, pry, prx,
-                             torch.cuda.current_stream().cuda_stream)
+                             _current_stream(dev))
     if rc:
         _check("dg_block_norm", rc)
     return res
@@ -739,12 +750,17 @@ def dg_block_norm_backward(dx_out: Optional[torch.Tensor], dh: Optional[torch.Te
     if given is None:
         raise ValueError("w_pre or w_post (with y) is needed")
     ptype, par = given.dtype, _dtype_of(given, "w_pre" if w_pre is not None else "w_post")
-    res, f32 = {}, torch.float32
+    res, f32, device = {}, torch.float32, x.device
 
     def new(key, dt, shp):
-        t = _given(out, key)
-        res[key] = t = torch.empty(shp, dtype=dt, device=x.device) if t is None else t
-        return _arg(t, f'out["{key}"]', dev, dt, shp)
+        t = None if out is None else out.get(key)
+        if t is not None:
+            p = _arg(t, key, dev, dt, shp)
+        else:
+            t = torch.empty_like(x, memory_format=torch.contiguous_format) if shp is shape else torch.empty(shp, dtype=dt, device=device)
+            p = t.data_ptr()
+        res[key] = t
+        return p
 
     pdo = pdh = px = py = pw = pg = pn = pry = prx = pdy = pdw = pdg = pdn = None
     ld_do = ld_dh = ld_x = ld_y = d
@@ -779,7 +795,7 @@ def dg_block_norm_backward(dx_out: Optional[torch.Tensor], dh: Optional[torch.Te
         raise ValueError("ws must be a contiguous tensor on the device of x")
     rc = L.dg_block_norm_backward(pdo, ld_do, pdh, ld_dh, px, ld_x, py, ld_y, act, pw, pg, pn, par, R // C, C, d, res_scale,
                                   pry, prx, pdx, pdy, pdw, pdg, pdn, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                  torch.cuda.current_stream().cuda_stream)
+                                  _current_stream(dev))
     if rc:
         _check("dg_block_norm_backward", rc)
     return res
@@ -809,7 +825,7 @@ def dg_mx4_quantize(x: torch.Tensor, *, out=None, stream=None):
     else:
         codes, scales = out
     rc = lib().dg_mx4_quantize(px, dt, ld, R, K, _arg(codes, "codes", dev, u8, (R, K // 2)),
-                               _arg(scales, "scales", dev, u8, scale_shape), torch.cuda.current_stream().cuda_stream)
+                               _arg(scales, "scales", dev, u8, scale_shape), _current_stream(dev))
     if rc:
         _check("dg_mx4_quantize", rc)
     return codes, scales
@@ -830,7 +846,7 @@ def dg_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, *, dtype: torch
         out = torch.empty((R, K), dtype=dtype, device=codes.device)
     rc = lib().dg_mx4_dequantize(_arg(codes, "codes", dev, u8, codes.shape), _arg(scales, "scales", dev, u8, dg_mx4_scale_shape(R, K)),
                                  R, K, _arg(out, "out", dev, dtype, (R, K)), _dtype_of(out, "out"),
-                                 torch.cuda.current_stream().cuda_stream)
+                                 _current_stream(dev))
     if rc:
         _check("dg_mx4_dequantize", rc)
     return out
@@ -857,7 +873,7 @@ def dg_mx4_matmul(a, w, *, dtype: torch.dtype = torch.bfloat16, out: Optional[to
     pa, psa = _mx4_arg(a, "a", dev, M, K)
     pw, psw = _mx4_arg(w, "w", dev, N, K)
     rc = lib().dg_mx4_matmul(pa, psa, pw, psw, M, N, K, _arg(out, "out", dev, dtype, (M, N)), _dtype_of(out, "out"),
-                             torch.cuda.current_stream().cuda_stream)
+                             _current_stream(dev))
     if rc:
         _check("dg_mx4_matmul", rc)
     return out
@@ -888,7 +904,7 @@ def dg_ffw_mx4(z: torch.Tensor, w1, w2, *, out: Optional[torch.Tensor] = None, w
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous tensor on the device of z")
     rc = L.dg_ffw_mx4(pz, R, d, dff, p1, ps1, p2, ps2, _arg(out, "out", dev, bf16, (R, d)), ws.data_ptr(),
-                      ws.numel() * ws.element_size(), torch.cuda.current_stream().cuda_stream)
+                      ws.numel() * ws.element_size(), _current_stream(dev))
     if rc:
         _check("dg_ffw_mx4", rc)
     return out

@@ -12,6 +12,7 @@
 // Padding in a tile (rows or blocks past the matrix) holds 127.
 #include <algorithm>
 #include <atomic>
+#include <cstdlib>
 #include <cstring>
 
 #include "common.cuh"
@@ -419,6 +420,358 @@ cudaError_t launch_product(const Mx4Kernel& kp, int grid, int splits, bool depen
     return cudaGetLastError();
 }
 
+// ------------------------------------------------------------------------------------ product, many tiles
+// The same product for many tiles: persistent clusters of two CTAs, each pair computing 256 rows x kN
+// columns at a time with tcgen05.mma.cta_group::2 (M = 256): a CTA stages its own 128 rows of A and
+// half of the W rows, so an operand byte read from L2 serves twice the products of a single CTA's tile;
+// the scales of W are staged by both, as both tensor memories hold them.  All copies of a stage
+// complete on the leader's barrier (box copies of cta_group::2, no multicast); the leader's MMA
+// thread commits a stage to both CTAs' empty barriers and a finished tile to both accumulator
+// barriers.  256 accumulator columns are two buffers of 128 or one of 256; eight epilogue warps
+// drain a buffer while the copies, and with two buffers the products, of the next tile run.
+template <int kN>
+struct PairTile {
+    static constexpr int kBuffers = 256 / kN;
+    static constexpr uint32_t kABytes = kOperandBytes;
+    static constexpr uint32_t kWBytes = (kN / 2) * (kKStage / 2);
+    static constexpr uint32_t kSwBytes = (kN / 128) * kScaleBytes;
+    static constexpr uint32_t kStage = kABytes + kWBytes + kScaleBytes + kSwBytes;
+    static constexpr uint32_t kSlabBytes = 16384;            // 128 rows x 128 bytes
+    static constexpr int kSlabs = kN / 128;                  // per epilogue group: its columns in bf16
+    static constexpr uint32_t kStaging = 2 * kSlabs * kSlabBytes;
+    static constexpr uint32_t kBudget = 226u * 1024u;
+    static constexpr int kFit = static_cast<int>((kBudget - kStaging) / kStage);
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
+    static constexpr uint32_t kSmem = kStaging + kStages * kStage + 512 + 1024;
+    static constexpr uint32_t kScaleCols = 8 + 8 * (kN / 128);  // of one stage: A, then W
+    static_assert(256 + kStages * kScaleCols <= 512, "accumulators and scales fit the tensor memory");
+    static_assert(kStage % 1024 == 0, "stages keep the 1024-byte alignment of the swizzle");
+    static_assert(kSmem <= 232448, "shared memory of a CTA");
+};
+constexpr int kPairThreads = 64 + 256;  // producer, MMA issuer, two groups of four epilogue warps
+
+struct alignas(64) Mx4PairKernel {
+    CUtensorMap tm_a, tm_w;    // bytes [rows, K / 2], boxes of 128 and kN / 2 rows x 128 bytes
+    CUtensorMap tm_sa, tm_sw;  // scale tiles as [tiles, 128] words, boxes of two tiles
+    CUtensorMap tm_out;        // bf16 (box 64 x 128) or fp32 (32 x 128) [M, N]
+    uint8_t* out_codes;        // kOutGeluMx4
+    uint8_t* out_scales;
+    int32_t M, N, K;
+    int32_t m_tiles, n_tiles, k_tiles, k_blocks;
+    long long wait_limit;
+};
+
+template <int kN>
+__device__ __forceinline__ uint32_t idesc_mx4_pair(uint32_t pair) {
+    return (pair << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kN >> 3) << 17) | (1u << 23) | (2u << 27) | (pair << 29);
+}
+__device__ __forceinline__ void umma_mx4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+// As copy_scales, in both CTAs of the pair: each from its own shared memory to its own tensor memory.
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint32_t smem_addr) {
+    const uint64_t d = smem_desc(smem_addr, 16, 128, 0);
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+}
+// Barrier of one epilogue group (128 threads) that also ORs a flag over it: one exit decision.
+__device__ __forceinline__ bool group_sync_or(int group, bool flag) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(flag)), "r"(1 + group)
+        : "memory");
+    return r != 0;
+}
+
+template <int kOut, int kN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    mx4_matmul_pair_kernel(const __grid_constant__ Mx4PairKernel p) {
+    using G = PairTile<kN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* staging = smem + G::kStages * G::kStage;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + G::kStaging);  // leader's: both CTAs' copies
+    uint64_t* empty = full + G::kStages;                                  // own stage free
+    uint64_t* acc_full = empty + G::kStages;                              // own accumulator buffer final
+    uint64_t* acc_empty = acc_full + G::kBuffers;                         // leader's: both CTAs drained the buffer
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + G::kBuffers);
+    WaitCtl* wc = reinterpret_cast<WaitCtl*>(tmem_slot + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int32_t tiles = p.m_tiles * p.n_tiles, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < G::kBuffers; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 16);  // eight epilogue warps in each CTA
+        }
+        wc->abort = 0;
+        wc->limit = p.wait_limit;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tcgen05_before_sync();
+    __syncthreads();
+    cluster_sync();  // barriers of both CTAs initialised before any remote arrival
+    tcgen05_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0 && lane == 0) {
+        // ---------------------------------------------------------------- producer (both CTAs)
+        const uint32_t leader_full = map_to_rank(smem_u32(&full[0]), 0);
+        grid_dependency_wait();  // A may be the preceding kernel's output
+        int i = 0;
+        bool ok = true;
+        for (int32_t t = first; ok && t < tiles; t += step) {
+            const int32_t nt = t / p.m_tiles, mt = t - nt * p.m_tiles;
+            const int32_t rt = 2 * mt + static_cast<int32_t>(rank);  // this CTA's group of 128 rows
+            for (int32_t kb = 0; kb < p.k_blocks; ++kb, ++i) {
+                const int s = i % G::kStages;
+                ok = mbar_wait(&empty[s], ((i / G::kStages) & 1) ^ 1, wc);
+                if (!ok) break;
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * G::kStage);
+                uint8_t* st = smem + s * G::kStage;
+                const uint32_t bar = leader_full + s * 8;
+                tma_load_2d_pair(st, &p.tm_a, kb * (kKStage / 2), rt * 128, bar);
+                tma_load_2d_pair(st + G::kABytes, &p.tm_w, kb * (kKStage / 2), nt * kN + static_cast<int32_t>(rank) * (kN / 2), bar);
+                uint8_t* sc = st + G::kABytes + G::kWBytes;
+                tma_load_2d_pair(sc, &p.tm_sa, 0, rt * p.k_tiles + 2 * kb, bar);
+#pragma unroll
+                for (int j = 0; j < kN / 128; ++j)
+                    tma_load_2d_pair(sc + kScaleBytes * (1 + j), &p.tm_sw, 0, (nt * (kN / 128) + j) * p.k_tiles + 2 * kb, bar);
+            }
+        }
+        if (aborted(wc) && rank == 0) {  // copies in flight land on the leader's barriers: wait for them (bounded)
+            const long long t0 = clock64();
+            for (int k = max(0, i - G::kStages); k < i; ++k)
+                while (!mbar_try_wait(&full[k % G::kStages], (k / G::kStages) & 1) && clock64() - t0 < wc->limit) {
+                }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---------------------------------------------------------------- MMA issuer (leader)
+        int i = 0, n = 0;
+        bool ok = true;
+        for (int32_t t = first; ok && t < tiles; t += step, ++n) {
+            const int b = n % G::kBuffers;
+            ok = mbar_wait(&acc_empty[b], ((n / G::kBuffers) & 1) ^ 1, wc);
+            if (!ok) break;
+            tcgen05_after_sync();
+            for (int32_t kb = 0; kb < p.k_blocks; ++kb, ++i) {
+                const int s = i % G::kStages;
+                ok = mbar_wait(&full[s], (i / G::kStages) & 1, wc);
+                if (!ok) break;
+                tcgen05_after_sync();
+                const uint32_t st = smem_u32(smem + s * G::kStage);
+                const uint32_t sc = st + G::kABytes + G::kWBytes;
+                const uint32_t sf = tmem + 256 + s * G::kScaleCols;  // A: 2 tiles x 4 columns; W: 2 x 4 kN / 128
+                const int32_t halves = min(2, p.k_tiles - 2 * kb);
+                for (int j = 0; j < halves; ++j) {
+                    copy_scales_pair(sf + 4 * j, sc + 512 * j);
+#pragma unroll
+                    for (int q = 0; q < kN / 128; ++q)
+                        copy_scales_pair(sf + 8 + (j * (kN / 128) + q) * 4, sc + kScaleBytes * (1 + q) + 512 * j);
+                }
+                const int32_t steps = min(4, (p.K - kb * kKStage + 63) / 64);
+                for (int ks = 0; ks < steps; ++ks)
+                    umma_mx4_pair(tmem + b * kN, smem_desc(st + ks * 32, 16, 1024, kLayoutSw128),
+                                  smem_desc(st + G::kABytes + ks * 32, 16, 1024, kLayoutSw128), idesc_mx4_pair<kN>((ks & 1) * 2),
+                                  sf + 4 * (ks >> 1), sf + 8 + (ks >> 1) * (kN / 128) * 4, (kb > 0 || ks > 0) ? 1u : 0u);
+                umma_commit_pair_both(smem_u32(&empty[s]));
+            }
+            if (ok) umma_commit_pair_both(smem_u32(&acc_full[b]));
+        }
+    } else if (warp >= 2) {
+        // ---------------------------------------------------------------- epilogue (both CTAs)
+        const int quarter = warp & 3, group = (warp - 2) >> 2;
+        const int row = quarter * 32 + lane;
+        const bool issuer = threadIdx.x == 64 + 128 * group;
+        const uint32_t leader_empty = map_to_rank(smem_u32(&acc_empty[0]), 0);
+        const uint32_t area = smem_u32(staging) + group * G::kSlabs * G::kSlabBytes;
+        const uint32_t row_base = area + row * 128;
+        const uint32_t sw = row & 7;
+        constexpr int kCols = kN / 2;  // of the group
+        int n = 0;
+        for (int32_t t = first; t < tiles; t += step, ++n) {
+            const int32_t nt = t / p.m_tiles, mt = t - nt * p.m_tiles;
+            const int b = n % G::kBuffers;
+            const bool got = mbar_wait(&acc_full[b], (n / G::kBuffers) & 1, wc);
+            if (issuer) bulk_wait_read_all();  // the slabs of the tile before have been read
+            if (group_sync_or(group, !got)) break;
+            tcgen05_after_sync();
+            const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * kN + group * kCols;
+            const int32_t row0 = (2 * mt + static_cast<int32_t>(rank)) * 128;
+            const int32_t col0 = nt * kN + group * kCols;
+            if (kOut == kOutGeluMx4) {
+                const bool valid = row0 + row < p.M;
+                const int64_t r = row0 + row;
+                uint32_t word = 0;
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(acc + c, v);
+                    uint32_t top = 0;
+                    float f[32];
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) {
+                        f[q] = gelu_exact(__uint_as_float(v[q]));
+                        top = max(top, __float_as_uint(f[q]) & 0x7FFFFFFFu);
+                    }
+                    const bool in = valid && col0 + c < p.N;
+                    const uint32_t sb = in ? scale_byte(top) : kUnitScale;
+                    if (in) {
+                        const float inv = inverse_scale(sb == 255u ? 127u : sb);
+                        uint32_t q4[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float(&g)[8] = *reinterpret_cast<const float(*)[8]>(&f[8 * q]);
+                            q4[q] = sb == 255u ? 0u : pack_e2m1(g, inv);
+                        }
+                        *reinterpret_cast<uint4*>(p.out_codes + r * (p.N / 2) + (col0 + c) / 2) = make_uint4(q4[0], q4[1], q4[2], q4[3]);
+                    }
+                    word |= sb << (8 * ((col0 + c) / 32 & 3));
+                    // whole tiles of 128 rows x 4 blocks; a group of 64 columns writes its half of the words
+                    if (kCols == 64 ? c == 32 : (c & 127) == 96) {
+                        const int32_t kt = (col0 + c) / 128, kts = (p.N + 127) / 128;
+                        if (kt < kts && row0 < (p.M + 127) / 128 * 128) {
+                            uint8_t* at = p.out_scales + (static_cast<int64_t>(row0 / 128) * kts + kt) * 512 + lane * 16 + quarter * 4;
+                            if (kCols == 64)
+                                *reinterpret_cast<uint16_t*>(at + 2 * group) = static_cast<uint16_t>(word >> (16 * group));
+                            else
+                                *reinterpret_cast<uint32_t*>(at) = word;
+                        }
+                        word = 0;
+                    }
+                }
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(leader_empty + b * 8);
+            } else {
+                constexpr int kSlabCols = kOut == kOutBf16 ? 64 : 32;
+                constexpr int kBatches = kCols / (kSlabCols * G::kSlabs) > 0 ? kCols / (kSlabCols * G::kSlabs) : 1;
+                constexpr int kSlabsUsed = kCols / (kSlabCols * kBatches);
+#pragma unroll 1
+                for (int batch = 0; batch < kBatches; ++batch) {
+                    if (batch > 0) {  // the previous batch has been read out before its slabs are overwritten
+                        if (issuer) bulk_wait_read_all();
+                        group_sync_or(group, false);
+                    }
+#pragma unroll
+                    for (int c = 0; c < kSlabsUsed * kSlabCols; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(acc + batch * kSlabsUsed * kSlabCols + c, v);
+                        const uint32_t slab = row_base + (c / kSlabCols) * G::kSlabBytes;
+                        if (kOut == kOutBf16) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                st_shared_v4(slab + ((((c & 32) / 8 + k) ^ sw) << 4),
+                                             make_uint4(pack_bf16x2(__uint_as_float(v[8 * k]), __uint_as_float(v[8 * k + 1])),
+                                                        pack_bf16x2(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3])),
+                                                        pack_bf16x2(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5])),
+                                                        pack_bf16x2(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7]))));
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                st_shared_v4(slab + ((k ^ sw) << 4), make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+                        }
+                    }
+                    if (batch == kBatches - 1) {  // the buffer is drained: the next tile's products may start
+                        tcgen05_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(leader_empty + b * 8);
+                    }
+                    fence_proxy_async_smem();
+                    group_sync_or(group, false);
+                    if (issuer && row0 < p.M) {
+#pragma unroll
+                        for (int j = 0; j < kSlabsUsed; ++j) {
+                            const int32_t col = col0 + (batch * kSlabsUsed + j) * kSlabCols;
+                            if (col < p.N) tma_store_2d(&p.tm_out, col, row0, area + j * G::kSlabBytes);
+                        }
+                        bulk_commit();
+                    }
+                }
+            }
+        }
+        if (issuer) bulk_wait_all();  // complete before the CTA may exit
+    }
+    __syncwarp();
+    grid_launch_dependents();
+    // neither CTA leaves (or frees its tensor memory) while its peer may still use it
+    tcgen05_before_sync();
+    __syncthreads();
+    cluster_sync();
+    tcgen05_after_sync();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+template <int kOut, int kN>
+cudaError_t launch_pair(const Mx4MatmulParams& q, cudaStream_t st) {
+    using G = PairTile<kN>;
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [] {
+        attr_err = cudaFuncSetAttribute(mx4_matmul_pair_kernel<kOut, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(G::kSmem));
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    Mx4PairKernel kp;
+    std::memset(&kp, 0, sizeof(kp));
+    kp.M = q.M;
+    kp.N = q.N;
+    kp.K = q.K;
+    kp.m_tiles = (q.M + 255) / 256;
+    kp.n_tiles = (q.N + kN - 1) / kN;
+    kp.k_tiles = (q.K + 127) / 128;
+    kp.k_blocks = (q.K + kKStage - 1) / kKStage;
+    kp.wait_limit = kWaitLimitCycles;
+    kp.out_codes = static_cast<uint8_t*>(q.out);
+    kp.out_scales = q.out_scales;
+    const uint64_t ta = static_cast<uint64_t>((q.M + 127) / 128) * kp.k_tiles, tw = static_cast<uint64_t>((q.N + 127) / 128) * kp.k_tiles;
+    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+    cudaError_t e = encode_2d(&kp.tm_a, u8, q.a, q.K / 2, q.M, q.K / 2, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess) e = encode_2d(&kp.tm_w, u8, q.w, q.K / 2, q.N, q.K / 2, 128, kN / 2, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess) e = encode_2d(&kp.tm_sa, u32, q.a_scales, 128, ta, 512, 128, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess) e = encode_2d(&kp.tm_sw, u32, q.w_scales, 128, tw, 512, 128, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess && kOut == kOutBf16)
+        e = encode_2d(&kp.tm_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q.out, q.N, q.M, static_cast<uint64_t>(q.N) * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess && kOut == kOutF32)
+        e = encode_2d(&kp.tm_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, q.out, q.N, q.M, static_cast<uint64_t>(q.N) * 4, 32, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = static_cast<int64_t>(kp.m_tiles) * kp.n_tiles;
+    if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, num_sms() / 2)));
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = G::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = q.dependent ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, mx4_matmul_pair_kernel<kOut, kN>, kp);
+    if (e != cudaSuccess) return e;
+    note_launches(1);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 size_t mx4_scale_bytes(int32_t rows, int32_t K) {
@@ -450,6 +803,14 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
 }
 
 cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
+    const int64_t pairs = static_cast<int64_t>((q.M + 255) / 256) * ((q.N + 127) / 128);
+    if (2 * pairs >= num_sms()) {
+        static const int force = getenv("MX4N") ? atoi(getenv("MX4N")) : 0;
+        const bool wide = force ? force == 256 : q.out_kind != kMx4OutGelu;
+        if (q.out_kind == kMx4OutF32) return wide ? launch_pair<kOutF32, 256>(q, st) : launch_pair<kOutF32, 128>(q, st);
+        if (q.out_kind == kMx4OutBf16) return wide ? launch_pair<kOutBf16, 256>(q, st) : launch_pair<kOutBf16, 128>(q, st);
+        return wide ? launch_pair<kOutGeluMx4, 256>(q, st) : launch_pair<kOutGeluMx4, 128>(q, st);
+    }
     Mx4Kernel kp;
     std::memset(&kp, 0, sizeof(kp));
     cudaError_t e = encode_2d(&kp.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.a, q.K / 2, q.M, q.K / 2, 128, kMTile, CU_TENSOR_MAP_SWIZZLE_128B);

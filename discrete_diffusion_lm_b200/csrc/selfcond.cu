@@ -388,15 +388,6 @@ struct PairCfg {
 
 constexpr int kPairThreads = 96 + 32 * kNumSoftmaxWarps;  // E producer, MMA/forwarder, logits producer
 
-// E box copy whose completion is counted on the pair leader's barrier.
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* tm, int32_t c0, int32_t c1,
-                                                 uint32_t leader_bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-        "%3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(tm), "r"(c0), "r"(c1), "r"(leader_bar)
-        : "memory");
-}
 __device__ __forceinline__ void umma_bf16_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                uint32_t accumulate) {
     asm volatile(
@@ -406,19 +397,6 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t tmem_d, uint64_t adesc, 
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void umma_commit_pair(uint32_t cluster_bar) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(cluster_bar)
-                 : "memory");
-}
-// One commit that arrives on the barrier at the same shared-memory offset in both CTAs of the pair
-// (own_bar: the executing CTA's shared-memory address of it).
-__device__ __forceinline__ void umma_commit_pair_both(uint32_t own_bar) {
-    const uint16_t mask = 0x3;
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(own_bar), "h"(mask)
-                 : "memory");
-}
-
 // Barrier among the four warps of one epilogue group (named barrier 3 + group, 128 threads).
 __device__ __forceinline__ void epilogue_group_bar(int group) {
     asm volatile("bar.sync %0, 128;" ::"r"(3 + group) : "memory");

@@ -272,7 +272,11 @@ def check_product(a, av, w, wv, dtype, **kw):
 
 @pytest.mark.parametrize("M,N,K", [(1, 8, 32), (128, 128, 256), (1, 128, 64), (7, 24, 96), (128, 128, 128), (129, 136, 160),
                                    (16, 256, 2048), (200, 1000, 4096), (300, 520, 544), (1, 2048, 8192), (64, 64, 2080),
-                                   (257, 384, 8192), (1000, 2056, 480)])
+                                   (257, 384, 8192), (1000, 2056, 480),
+                                   # many tiles: ragged rows and columns, one row in the last pair of row tiles, K ending in
+                                   # every part of a stage, more tiles than pairs of CTAs
+                                   (2048, 2056, 480), (257, 9608, 96), (4000, 1288, 1184), (2000, 4096, 2048), (2305, 2312, 320),
+                                   (5000, 3000, 64), (4096, 2048, 800)])
 def test_product(M, N, K):
     g = gen(M + N + K)
     (a, av), (w, wv) = random_mx4(g, M, K), random_mx4(g, N, K)
@@ -345,7 +349,7 @@ def check_block(z, w1, w1v, w2, w2v, got):
     return (slack > 0).double().mean().item()
 
 
-@pytest.mark.parametrize("R,d,dff", [(1, 64, 64), (16, 64, 256), (5, 192, 320), (1, 1024, 4096), (130, 512, 2048), (256, 2048, 8192), (300, 128, 576)])
+@pytest.mark.parametrize("R,d,dff", [(1, 64, 64), (16, 64, 256), (5, 192, 320), (1, 1024, 4096), (130, 512, 2048), (256, 2048, 8192), (300, 128, 576), (2500, 320, 2112), (1100, 1024, 4096)])
 def test_block(R, d, dff):
     g = gen(R + d)
     z = randn(g, R, d, dtype=BF16)
