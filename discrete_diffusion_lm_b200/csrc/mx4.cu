@@ -448,7 +448,7 @@ struct PairTile {
     static_assert(kStage % 1024 == 0, "stages keep the 1024-byte alignment of the swizzle");
     static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
-constexpr int kPairThreads = 64 + 256;  // producer, MMA issuer, two groups of four epilogue warps
+constexpr int kPairThreads = 64 + 256 + 32;  // producer, MMA issuer, two groups of four epilogue warps, scale copies
 
 struct alignas(64) Mx4PairKernel {
     CUtensorMap tm_a, tm_w;    // bytes [rows, K / 2], boxes of 128 and kN / 2 rows x 128 bytes
@@ -475,9 +475,29 @@ __device__ __forceinline__ void umma_mx4_pair(uint32_t d, uint64_t a, uint64_t b
         : "memory");
 }
 // As copy_scales, in both CTAs of the pair: each from its own shared memory to its own tensor memory.
-__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint32_t smem_addr) {
-    const uint64_t d = smem_desc(smem_addr, 16, 128, 0);
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint64_t d) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x32_nowait(uint32_t taddr, uint32_t* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
 }
 // Barrier of one epilogue group (128 threads) that also ORs a flag over it: one exit decision.
 __device__ __forceinline__ bool group_sync_or(int group, bool flag) {
@@ -502,7 +522,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint8_t* staging = smem + G::kStages * G::kStage;
     uint64_t* full = reinterpret_cast<uint64_t*>(staging + G::kStaging);  // leader's: both CTAs' copies
     uint64_t* empty = full + G::kStages;                                  // own stage free
-    uint64_t* acc_full = empty + G::kStages;                              // own accumulator buffer final
+    uint64_t* scaled = empty + G::kStages;                                // leader's: scales in both tensor memories
+    uint64_t* acc_full = scaled + G::kStages;                             // own accumulator buffer final
     uint64_t* acc_empty = acc_full + G::kBuffers;                         // leader's: both CTAs drained the buffer
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + G::kBuffers);
     WaitCtl* wc = reinterpret_cast<WaitCtl*>(tmem_slot + 2);
@@ -514,6 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (int s = 0; s < G::kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&scaled[s], 1);
         }
         for (int b = 0; b < G::kBuffers; ++b) {
             mbar_init(&acc_full[b], 1);
@@ -564,38 +586,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 while (!mbar_try_wait(&full[k % G::kStages], (k / G::kStages) & 1) && clock64() - t0 < wc->limit) {
                 }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         // ---------------------------------------------------------------- MMA issuer (leader)
-        int i = 0, n = 0;
+        // The whole warp walks the loop, so that addresses and descriptors stay in uniform registers, and
+        // one elected lane issues: a product is issued in fewer cycles than the 128 it takes.
+        const uint64_t da0 = smem_desc(smem_u32(smem), 16, 1024, kLayoutSw128);
+        const uint64_t dw0 = smem_desc(smem_u32(smem) + G::kABytes, 16, 1024, kLayoutSw128);
+        int s = 0, phase = 0, n = 0;
         bool ok = true;
         for (int32_t t = first; ok && t < tiles; t += step, ++n) {
             const int b = n % G::kBuffers;
-            ok = mbar_wait(&acc_empty[b], ((n / G::kBuffers) & 1) ^ 1, wc);
+            ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[b], ((n / G::kBuffers) & 1) ^ 1, wc));
             if (!ok) break;
             tcgen05_after_sync();
-            for (int32_t kb = 0; kb < p.k_blocks; ++kb, ++i) {
-                const int s = i % G::kStages;
-                ok = mbar_wait(&full[s], (i / G::kStages) & 1, wc);
+            const uint32_t acc = tmem + b * kN;
+            for (int32_t kb = 0; kb < p.k_blocks; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&scaled[s], phase, wc));
                 if (!ok) break;
                 tcgen05_after_sync();
-                const uint32_t st = smem_u32(smem + s * G::kStage);
-                const uint32_t sc = st + G::kABytes + G::kWBytes;
+                const uint64_t da = da0 + static_cast<uint64_t>(s * (G::kStage / 16)), dw = dw0 + static_cast<uint64_t>(s * (G::kStage / 16));
                 const uint32_t sf = tmem + 256 + s * G::kScaleCols;  // A: 2 tiles x 4 columns; W: 2 x 4 kN / 128
-                const int32_t halves = min(2, p.k_tiles - 2 * kb);
-                for (int j = 0; j < halves; ++j) {
-                    copy_scales_pair(sf + 4 * j, sc + 512 * j);
-#pragma unroll
-                    for (int q = 0; q < kN / 128; ++q)
-                        copy_scales_pair(sf + 8 + (j * (kN / 128) + q) * 4, sc + kScaleBytes * (1 + q) + 512 * j);
-                }
+                const uint32_t bar = smem_u32(&empty[s]), done = smem_u32(&acc_full[b]);
                 const int32_t steps = min(4, (p.K - kb * kKStage + 63) / 64);
-                for (int ks = 0; ks < steps; ++ks)
-                    umma_mx4_pair(tmem + b * kN, smem_desc(st + ks * 32, 16, 1024, kLayoutSw128),
-                                  smem_desc(st + G::kABytes + ks * 32, 16, 1024, kLayoutSw128), idesc_mx4_pair<kN>((ks & 1) * 2),
-                                  sf + 4 * (ks >> 1), sf + 8 + (ks >> 1) * (kN / 128) * 4, (kb > 0 || ks > 0) ? 1u : 0u);
-                umma_commit_pair_both(smem_u32(&empty[s]));
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        if (ks < steps)
+                            umma_mx4_pair(acc, da + 2 * ks, dw + 2 * ks, idesc_mx4_pair<kN>((ks & 1) * 2), sf + 4 * (ks >> 1),
+                                          sf + 8 + (ks >> 1) * (kN / 128) * 4, (kb > 0 || ks > 0) ? 1u : 0u);
+                    umma_commit_pair_both(bar);
+                    if (kb == p.k_blocks - 1) umma_commit_pair_both(done);
+                }
+                __syncwarp();
+                if (++s == G::kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
-            if (ok) umma_commit_pair_both(smem_u32(&acc_full[b]));
+        }
+    } else if (warp == 10) {
+        // ---------------------------------------------------------------- scale copies (leader)
+        // A thread of their own: tcgen05.cp and the products that follow it in one thread run one after
+        // the other, which cost 1300 cycles per stage against the products' 512.
+        if (rank == 0) {
+            const uint64_t d0 = smem_desc(smem_u32(smem) + G::kABytes + G::kWBytes, 16, 128, 0);
+            const uint32_t own_scaled = map_to_rank(smem_u32(&scaled[0]), 0);
+            int s = 0, phase = 0;
+            bool ok = true;
+            for (int32_t t = first; ok && t < tiles; t += step) {
+                for (int32_t kb = 0; kb < p.k_blocks; ++kb) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&full[s], phase, wc));
+                    if (!ok) break;
+                    tcgen05_after_sync();
+                    const uint64_t d = d0 + static_cast<uint64_t>(s * (G::kStage / 16));
+                    const uint32_t sf = tmem + 256 + s * G::kScaleCols, bar = own_scaled + s * 8;
+                    const int32_t halves = min(2, p.k_tiles - 2 * kb);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (j < halves) {
+                                copy_scales_pair(sf + 4 * j, d + 32 * j);
+#pragma unroll
+                                for (int q = 0; q < kN / 128; ++q)
+                                    copy_scales_pair(sf + 8 + (j * (kN / 128) + q) * 4, d + 64 * (1 + q) + 32 * j);
+                            }
+                        umma_commit_pair(bar);
+                    }
+                    __syncwarp();
+                    if (++s == G::kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
         }
     } else if (warp >= 2) {
         // ---------------------------------------------------------------- epilogue (both CTAs)
@@ -666,7 +729,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 constexpr int kSlabCols = kOut == kOutBf16 ? 64 : 32;
                 constexpr int kBatches = kCols / (kSlabCols * G::kSlabs) > 0 ? kCols / (kSlabCols * G::kSlabs) : 1;
                 constexpr int kSlabsUsed = kCols / (kSlabCols * kBatches);
-#pragma unroll 1
+                // the whole share of the accumulator goes to registers first: the next tile's products wait
+                // only for that
+                uint32_t v[kCols];
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) tmem_ld_32x32b_x32_nowait(acc + c, v + c);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(leader_empty + b * 8);
+#pragma unroll
                 for (int batch = 0; batch < kBatches; ++batch) {
                     if (batch > 0) {  // the previous batch has been read out before its slabs are overwritten
                         if (issuer) bulk_wait_read_all();
@@ -674,27 +746,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     }
 #pragma unroll
                     for (int c = 0; c < kSlabsUsed * kSlabCols; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(acc + batch * kSlabsUsed * kSlabCols + c, v);
+                        const uint32_t* w = v + batch * kSlabsUsed * kSlabCols + c;
                         const uint32_t slab = row_base + (c / kSlabCols) * G::kSlabBytes;
                         if (kOut == kOutBf16) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 st_shared_v4(slab + ((((c & 32) / 8 + k) ^ sw) << 4),
-                                             make_uint4(pack_bf16x2(__uint_as_float(v[8 * k]), __uint_as_float(v[8 * k + 1])),
-                                                        pack_bf16x2(__uint_as_float(v[8 * k + 2]), __uint_as_float(v[8 * k + 3])),
-                                                        pack_bf16x2(__uint_as_float(v[8 * k + 4]), __uint_as_float(v[8 * k + 5])),
-                                                        pack_bf16x2(__uint_as_float(v[8 * k + 6]), __uint_as_float(v[8 * k + 7]))));
+                                             make_uint4(pack_bf16x2(__uint_as_float(w[8 * k]), __uint_as_float(w[8 * k + 1])),
+                                                        pack_bf16x2(__uint_as_float(w[8 * k + 2]), __uint_as_float(w[8 * k + 3])),
+                                                        pack_bf16x2(__uint_as_float(w[8 * k + 4]), __uint_as_float(w[8 * k + 5])),
+                                                        pack_bf16x2(__uint_as_float(w[8 * k + 6]), __uint_as_float(w[8 * k + 7]))));
                         } else {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                st_shared_v4(slab + ((k ^ sw) << 4), make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+                                st_shared_v4(slab + ((k ^ sw) << 4), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
                         }
-                    }
-                    if (batch == kBatches - 1) {  // the buffer is drained: the next tile's products may start
-                        tcgen05_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_remote(leader_empty + b * 8);
                     }
                     fence_proxy_async_smem();
                     group_sync_or(group, false);
