@@ -27,7 +27,7 @@ constexpr uint32_t kUnitScale = 127;  // the scale byte of 2^0
 
 // The scale byte of a block whose largest magnitude has the bit pattern `top` (sign cleared).
 __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
-    if (top >= 0x7F800000u) return 255u;
+    if (top >= 0x7F800000u) return 255u;  // an infinity, or a NaN of either sign
     const uint32_t ex = top >> 23;  // biased exponent; 0 for zero and subnormal values, whose e is -127
     return ex > 2u ? ex - 2u : 0u;
 }
@@ -213,11 +213,23 @@ __device__ __forceinline__ uint32_t cluster_size() {
 
 // GELU, tanh form, as x / (1 + exp(-2u)): the hidden layer is rounded to 4 bits by comparisons with
 // the E2M1 midpoints, so an error here moves values across them; the hardware tanh's 2^-11 would
-// move one value in a few hundred, ex2 and a division (about 2^-22) one in a million.
+// move one value in a few hundred, ex2 and a reciprocal (about 2^-22) one in a million.  u is kept
+// below 2^7, where the quotient is under 2^-100 and the reciprocal still a normal number.
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float gelu_exact(float x) {
-    const float k = -2.0f * 0.7978845608028654f * kLog2e;  // -2 sqrt(2 / pi) log2 e
-    const float u = k * fmaf(0.044715f * x, x * x, x);
-    return __fdividef(x, 1.0f + exp2f(fminf(u, 126.0f)));
+    const float k0 = -2.0f * 0.7978845608028654f * kLog2e;  // -2 sqrt(2 / pi) log2 e
+    const float u = x * fmaf(k0 * 0.044715f, x * x, k0);
+    return x * rcp_approx(1.0f + ex2_approx(fminf(u, 125.0f)));
+}
+// max(a, |b|) that keeps a NaN.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
 }
 
 template <int kOut>
@@ -366,9 +378,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid
         } else {
             // eight lanes hold a block of 32 hidden values
             const float f[4] = {gelu_exact(v.x), gelu_exact(v.y), gelu_exact(v.z), gelu_exact(v.w)};
-            uint32_t top = 0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) top = max(top, __float_as_uint(f[q]) & 0x7FFFFFFFu);
+            uint32_t top = __float_as_uint(max_abs_nan(max_abs_nan(max_abs_nan(fabsf(f[0]), f[1]), f[2]), f[3]));
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
             const bool in = i < m_valid && col < p.N;
@@ -689,13 +699,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 for (int c = 0; c < kCols; c += 32) {
                     uint32_t v[32];
                     tmem_ld_32x32b_x32(acc + c, v);
-                    uint32_t top = 0;
-                    float f[32];
+                    float f[32], most[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int q = 0; q < 32; ++q) {
                         f[q] = gelu_exact(__uint_as_float(v[q]));
-                        top = max(top, __float_as_uint(f[q]) & 0x7FFFFFFFu);
+                        most[q & 3] = max_abs_nan(most[q & 3], f[q]);
                     }
+                    const uint32_t top = __float_as_uint(max_abs_nan(max_abs_nan(most[0], most[1]), max_abs_nan(most[2], most[3])));
                     const bool in = valid && col0 + c < p.N;
                     const uint32_t sb = in ? scale_byte(top) : kUnitScale;
                     if (in) {
@@ -768,9 +778,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                         for (int j = 0; j < kSlabsUsed; ++j) {
                             const int32_t col = col0 + (batch * kSlabsUsed + j) * kSlabCols;
-                            if (col < p.N) tma_store_2d(&p.tm_out, col, row0, area + j * G::kSlabBytes);
+                            if (col >= p.N) break;
+#pragma unroll 1
+                            for (int q = 0; q < 4 && row0 + 32 * q < p.M; ++q) {
+                                tma_store_2d(&p.tm_out, col, row0 + 32 * q, area + j * G::kSlabBytes + q * 4096);
+                                bulk_commit();
+                                bulk_wait_read_all();
+                            }
                         }
-                        bulk_commit();
                     }
                 }
             }
@@ -816,9 +831,9 @@ cudaError_t launch_pair(const Mx4MatmulParams& q, cudaStream_t st) {
     if (e == cudaSuccess) e = encode_2d(&kp.tm_sa, u32, q.a_scales, 128, ta, 512, 128, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e == cudaSuccess) e = encode_2d(&kp.tm_sw, u32, q.w_scales, 128, tw, 512, 128, 2, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e == cudaSuccess && kOut == kOutBf16)
-        e = encode_2d(&kp.tm_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q.out, q.N, q.M, static_cast<uint64_t>(q.N) * 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+        e = encode_2d(&kp.tm_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q.out, q.N, q.M, static_cast<uint64_t>(q.N) * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e == cudaSuccess && kOut == kOutF32)
-        e = encode_2d(&kp.tm_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, q.out, q.N, q.M, static_cast<uint64_t>(q.N) * 4, 32, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+        e = encode_2d(&kp.tm_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, q.out, q.N, q.M, static_cast<uint64_t>(q.N) * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
     const int64_t tiles = static_cast<int64_t>(kp.m_tiles) * kp.n_tiles;
     if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
