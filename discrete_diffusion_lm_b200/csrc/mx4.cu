@@ -12,7 +12,6 @@
 // Padding in a tile (rows or blocks past the matrix) holds 127.
 #include <algorithm>
 #include <atomic>
-#include <cstdlib>
 #include <cstring>
 
 #include "common.cuh"
@@ -146,22 +145,27 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* __re
 //
 // A CTA computes 128 rows x 128 columns over a run of 256-value blocks of K.  Per block, one thread
 // copies the W tile (128-byte rows, 128-byte swizzle) and its scale tiles, another the A tile and
-// its scale tiles (it waits for the preceding kernel first: A may be that kernel's output); the
-// MMA thread moves the scales into tensor memory (tcgen05.cp) and issues four
-// tcgen05.mma.kind::mxf4 of K = 64, two scale bytes per row and instruction.
-// With few tiles K is split over the CTAs of a cluster: each leaves its fp32 tile in shared memory
-// and the CTAs add the tiles, each a share of the rows, in a fixed order.
+// its scale tiles (it waits for the preceding kernel first: A may be that kernel's output); a third
+// moves the scales into tensor memory (tcgen05.cp), and a fourth issues four
+// tcgen05.mma.kind::mxf4 of K = 64, two scale bytes per row and instruction.  (tcgen05.cp and the
+// products that follow it in one thread run one after the other: with both in one thread a stage took
+// 1100 to 1300 cycles instead of about 560.)
+// With few tiles K is split over the CTAs of a cluster: each sends every other its share of the rows
+// of its fp32 tile (bulk copies into that CTA's inbox), and adds the shares it is sent in a fixed order.
 constexpr int kMTile = 128, kNTile = 128, kKStage = 256;
-constexpr int kMx4Threads = 192;  // W producer, MMA issuer, four epilogue warps (the first also copies A)
+constexpr int kMx4Threads = 384;  // W copies, products, A copies, scale copies; eight epilogue warps
 constexpr uint32_t kOperandBytes = 128 * kKStage / 2;
 constexpr uint32_t kScaleBytes = 1024;  // two tiles
 constexpr uint32_t kStageBytes = 2 * (kOperandBytes + kScaleBytes);
-constexpr int kMx4Stages = 6;
+constexpr int kMx4Stages = 6;       // of the ring; a split of K keeps kSplitStages and has the rest as inbox
+constexpr int kSplitStages = 4;
 constexpr uint32_t kTmemCols = 256;  // 128 accumulator columns, 16 per stage of scales
 constexpr int kTilePitch = kNTile + 4;  // floats; rows 16 bytes off the banks of the row before
-constexpr uint32_t kMx4Smem = kMx4Stages * kStageBytes + 256 + 1024;
+constexpr uint32_t kMx4Smem = kMx4Stages * kStageBytes + 512 + 1024;
 static_assert(kMx4Stages * 16 + kNTile <= static_cast<int>(kTmemCols), "scales and accumulator fit");
-static_assert(kMTile * kTilePitch * 4 <= kMx4Stages * kStageBytes, "the fp32 tile fits the drained ring");
+static_assert(kMTile * kTilePitch * 4 <= kSplitStages * kStageBytes, "the fp32 tile fits the drained ring");
+// an inbox holds splits - 1 shares of up to 128 / splits rows: 3 x 32 or 64
+static_assert(3 * 32 * kTilePitch * 4 <= (kMx4Stages - kSplitStages) * kStageBytes, "the inbox fits the rest");
 
 enum Mx4Out : int { kOutBf16 = 0, kOutF32 = 1, kOutGeluMx4 = 2 };
 
@@ -190,9 +194,19 @@ __device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uin
         "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
         : "memory");
 }
-// 32 rows x 16 bytes of shared memory to four tensor-memory columns, repeated for the four lane groups.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem_addr) {
-    const uint64_t d = smem_desc(smem_addr, 16, 128, 0);  // no swizzle, groups of 8 rows 128 bytes apart
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+// 32 rows x 16 bytes of shared memory (no swizzle, groups of 8 rows 128 bytes apart) to four
+// tensor-memory columns, repeated for the four lane groups.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t d) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -200,11 +214,15 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
+// Shared memory of this CTA to another CTA's of the cluster, counted on that CTA's barrier.
+__device__ __forceinline__ void bulk_send(uint32_t dst_cluster, uint32_t src, uint32_t bytes, uint32_t bar_cluster) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst_cluster),
+                 "r"(src), "r"(bytes), "r"(bar_cluster)
+                 : "memory");
 }
+// (relaxed: mbarrier initialisation is released by its own fence, shares by the barrier they complete on)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
@@ -237,167 +255,230 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kMx4Stages * kStageBytes);
-    uint64_t* empty = full + kMx4Stages;
+    uint64_t* scaled = full + kMx4Stages;
+    uint64_t* empty = scaled + kMx4Stages;
     uint64_t* accum = empty + kMx4Stages;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accum + 1);
+    uint64_t* inbox_full = accum + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(inbox_full + 1);
     WaitCtl* wc = reinterpret_cast<WaitCtl*>(tmem_slot + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t splits = cluster_size(), split = cluster_rank();
+    const int splits = static_cast<int>(cluster_size()), split = static_cast<int>(cluster_rank());
+    const int stages = splits > 1 ? kSplitStages : kMx4Stages;
     const int32_t tile = blockIdx.x / splits;
     const int32_t mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
     const int32_t kb0 = static_cast<int32_t>(static_cast<int64_t>(p.k_blocks) * split / splits);
     const int32_t kb1 = static_cast<int32_t>(static_cast<int64_t>(p.k_blocks) * (split + 1) / splits);
+    const int32_t m_valid = min(kMTile, p.M - mt * kMTile);
+    const int32_t share = (m_valid + splits - 1) / splits;  // rows of the tile that a split adds up
 
+    // one stage's copy of an operand: W (or A) rows and their scale tiles
+    const auto load_stage = [&](int32_t kb, int s, bool is_a) {
+        const int32_t rt = is_a ? mt : nt;
+        uint8_t* st = smem + s * kStageBytes;
+        uint64_t* bar = &full[s];
+        const uint32_t scale_bytes = min(2, p.k_tiles - 2 * kb) * 512;
+        mbar_arrive_expect_tx(bar, kOperandBytes + scale_bytes);
+        tma_load_2d(st + (is_a ? 0 : kOperandBytes), is_a ? &p.tm_a : &p.tm_w, kb * (kKStage / 2), rt * 128, bar);
+        bulk_load(st + 2 * kOperandBytes + (is_a ? 0 : kScaleBytes),
+                  (is_a ? p.sa : p.sw) + static_cast<int64_t>(rt) * p.k_tiles * 512 + static_cast<int64_t>(kb) * 1024, scale_bytes, bar);
+    };
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMx4Stages; ++s) {
             mbar_init(&full[s], 2);
+            mbar_init(&scaled[s], 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(accum, 1);
+        mbar_init(inbox_full, 1);
         wc->abort = 0;
         wc->limit = p.wait_limit;
         fence_barrier_init();
     }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    tcgen05_before_sync();
     __syncthreads();
-    tcgen05_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    if (splits > 1) cluster_arrive();  // this CTA's inbox barrier is initialised
+    // The copies start at once; the warps that use the tensor memory meet when it is there.
+    if (warp != 0 && warp != 2) {
+        if (warp == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+        tcgen05_before_sync();
+        asm volatile("bar.sync 1, %0;" ::"n"(kMx4Threads - 64) : "memory");
+        tcgen05_after_sync();
+    }
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
     if ((warp == 0 || warp == 2) && lane == 0) {
         // ---------------------------------------------------------------- producers: W, A
         const bool is_a = warp == 2;
-        const CUtensorMap* tm = is_a ? &p.tm_a : &p.tm_w;
-        const int32_t rt = is_a ? mt : nt;
-        const uint8_t* scales = (is_a ? p.sa : p.sw) + static_cast<int64_t>(rt) * p.k_tiles * 512;
-        const uint32_t offset = is_a ? 0 : kOperandBytes;
-        const uint32_t scale_offset = 2 * kOperandBytes + (is_a ? 0 : kScaleBytes);
-        if (is_a) grid_dependency_wait();
         int32_t kb = kb0;
-        for (; kb < kb1; ++kb) {
-            const int i = kb - kb0, s = i % kMx4Stages;
-            if (!mbar_wait(&empty[s], ((i / kMx4Stages) & 1) ^ 1, wc)) break;
-            uint8_t* st = smem + s * kStageBytes;
-            const uint32_t scale_bytes = min(2, p.k_tiles - 2 * kb) * 512;
-            mbar_arrive_expect_tx(&full[s], kOperandBytes + scale_bytes);
-            tma_load_2d(st + offset, tm, kb * (kKStage / 2), rt * 128, &full[s]);
-            bulk_load(st + scale_offset, scales + static_cast<int64_t>(kb) * 1024, scale_bytes, &full[s]);
+        if (is_a) grid_dependency_wait();  // A may be the preceding kernel's output; the weights are not
+        for (int s = 0, phase = 0; kb < kb1; ++kb) {
+            if (s == stages) {
+                s = 0;
+                phase ^= 1;
+            }
+            if (!mbar_wait(&empty[s], phase ^ 1, wc)) break;
+            load_stage(kb, s++, is_a);
         }
         if (aborted(wc)) {  // let the copies in flight land before the shared memory goes away
             const long long t0 = clock64();
-            for (int i = max(0, kb - kb0 - kMx4Stages); i < kb - kb0; ++i)
-                while (!mbar_try_wait(&full[i % kMx4Stages], (i / kMx4Stages) & 1) && clock64() - t0 < wc->limit) {
+            for (int i = max(0, kb - kb0 - stages); i < kb - kb0; ++i)
+                while (!mbar_try_wait(&full[i % stages], (i / stages) & 1) && clock64() - t0 < wc->limit) {
                 }
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
+        // The whole warp walks the loop, so that descriptors stay in uniform registers; one lane issues.
+        const uint64_t da0 = smem_desc(smem_u32(smem), 16, 1024, kLayoutSw128);
+        int s = 0, phase = 0;
         for (int32_t kb = kb0; kb < kb1; ++kb) {
-            const int i = kb - kb0, s = i % kMx4Stages;
-            if (!mbar_wait(&full[s], (i / kMx4Stages) & 1, wc)) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&scaled[s], phase, wc))) break;
             tcgen05_after_sync();
-            const uint32_t st = smem_u32(smem + s * kStageBytes);
+            const uint64_t da = da0 + static_cast<uint64_t>(s * (kStageBytes / 16)), dw = da + kOperandBytes / 16;
             const uint32_t sf = tmem + kNTile + s * 16;  // two tiles of A, two of W, four columns each
-            const int32_t tiles = min(2, p.k_tiles - 2 * kb);
-            for (int j = 0; j < tiles; ++j) {
-                copy_scales(sf + 4 * j, st + 2 * kOperandBytes + 512 * j);
-                copy_scales(sf + 8 + 4 * j, st + 2 * kOperandBytes + kScaleBytes + 512 * j);
-            }
             const int32_t steps = min(4, (p.K - kb * kKStage + 63) / 64);
-            for (int ks = 0; ks < steps; ++ks)
-                umma_mx4(tmem, smem_desc(st + ks * 32, 16, 1024, kLayoutSw128),
-                         smem_desc(st + kOperandBytes + ks * 32, 16, 1024, kLayoutSw128), idesc_mx4((ks & 1) * 2),
-                         sf + 4 * (ks >> 1), sf + 8 + 4 * (ks >> 1), (i > 0 || ks > 0) ? 1u : 0u);
-            umma_commit(&empty[s]);
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    if (ks < steps)
+                        umma_mx4(tmem, da + 2 * ks, dw + 2 * ks, idesc_mx4((ks & 1) * 2), sf + 4 * (ks >> 1), sf + 8 + 4 * (ks >> 1),
+                                 (kb > kb0 || ks > 0) ? 1u : 0u);
+                umma_commit(&empty[s]);
+                if (kb == kb1 - 1) umma_commit(accum);
+            }
+            __syncwarp();
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1;
+            }
         }
-        umma_commit(accum);
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- scale copies
+        const uint64_t d0 = smem_desc(smem_u32(smem) + 2 * kOperandBytes, 16, 128, 0);
+        int s = 0, phase = 0;
+        for (int32_t kb = kb0; kb < kb1; ++kb) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[s], phase, wc))) break;
+            tcgen05_after_sync();
+            const uint64_t d = d0 + static_cast<uint64_t>(s * (kStageBytes / 16));
+            const uint32_t sf = tmem + kNTile + s * 16;
+            const int32_t tiles = min(2, p.k_tiles - 2 * kb);
+            if (elect_one()) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (j < tiles) {
+                        copy_scales(sf + 4 * j, d + 32 * j);
+                        copy_scales(sf + 8 + 4 * j, d + kScaleBytes / 16 + 32 * j);
+                    }
+                umma_commit(&scaled[s]);
+            }
+            __syncwarp();
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1;
+            }
+        }
     }
     __syncwarp();
 
     // ---------------------------------------------------------------- epilogue: fp32 tile, then rows
-    const int32_t m_valid = min(kMTile, p.M - mt * kMTile);
     float* tile_f = reinterpret_cast<float*>(smem);
     bool ok = true;
-    if (warp >= 2) {
+    if (warp >= 4) {
         ok = __all_sync(0xffffffffu, mbar_wait(accum, 0, wc));
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
         if (ok && quarter * 32 < m_valid) {
             tcgen05_after_sync();
             const int row = quarter * 32 + lane;
+            const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * (kNTile / 2);
+            uint32_t v[64];
+            tmem_ld_32x32b_x32_nowait(acc, v);
+            tmem_ld_32x32b_x32_nowait(acc + 32, v + 32);
+            tmem_ld_wait();
+            if (row < m_valid) {  // rows of kTilePitch floats
+                const uint32_t at = smem_u32(tile_f + row * kTilePitch + half * (kNTile / 2));
 #pragma unroll
-            for (int c = 0; c < kNTile; c += 32) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, v);
-                if (row < m_valid) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        st_shared_v4(smem_u32(tile_f + row * kTilePitch + c + 4 * q), make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
-                }
+                for (int q = 0; q < 16; ++q) st_shared_v4(at + 16 * q, make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
             }
         }
     }
     grid_launch_dependents();
+    if (splits > 1) fence_proxy_async_smem();  // the tile's rows, visible to the bulk copies
     ok = __syncthreads_and(ok);
-    if (splits > 1) cluster_sync();  // every split's tile is in place
-    const int32_t n0 = nt * kNTile;
-    const int32_t col = n0 + lane * 4;
-    // rows split, split + splits, ... of the tile, over the CTA's six warps; a lane takes four columns
-    const int32_t last = kOut == kOutGeluMx4 ? kMTile : m_valid;  // whole scale tiles
-    for (int32_t i = split + splits * warp; ok && i < last; i += splits * (kMx4Threads / 32)) {
-        const int64_t r = static_cast<int64_t>(mt) * kMTile + i;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < m_valid) {
-            const uint32_t at = smem_u32(tile_f + i * kTilePitch + lane * 4);
-            if (splits == 1) {
-                v = *reinterpret_cast<const float4*>(tile_f + i * kTilePitch + lane * 4);
-            } else {
-                float4 w[8];
-#pragma unroll
-                for (uint32_t s = 0; s < 8; ++s)
-                    if (s < splits) w[s] = ld_cluster_f4(map_to_rank(at, s));
-                v = w[0];
-#pragma unroll
-                for (uint32_t s = 1; s < 8; ++s)
-                    if (s < splits) {
-                        v.x += w[s].x;
-                        v.y += w[s].y;
-                        v.z += w[s].z;
-                        v.w += w[s].w;
-                    }
+    const int32_t row0 = min(split * share, m_valid), rows = min(share, m_valid - row0);
+    float* inbox = reinterpret_cast<float*>(smem + kSplitStages * kStageBytes);  // (splits - 1) shares
+    if (splits > 1) {
+        cluster_wait();  // every inbox barrier is initialised
+        if (warp == 0 && elect_one()) {
+            mbar_arrive_expect_tx(inbox_full, static_cast<uint32_t>((splits - 1) * rows * kTilePitch * 4));
+            for (int d = 1; d < splits; ++d) {  // to split `to`, its share; slots are in the order of the senders
+                const int to = (split + d) % splits;
+                const int32_t first = min(to * share, m_valid), n = min(share, m_valid - first);
+                if (n > 0)
+                    bulk_send(map_to_rank(smem_u32(inbox + (split < to ? split : split - 1) * n * kTilePitch), to),
+                              smem_u32(tile_f + first * kTilePitch), static_cast<uint32_t>(n * kTilePitch * 4), map_to_rank(smem_u32(inbox_full), to));
             }
         }
-        if (kOut == kOutF32) {
-            if (col < p.N) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + r * p.N + col) = v;
-        } else if (kOut == kOutBf16) {
-            if (col < p.N)
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + r * p.N + col) =
-                    make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-        } else {
-            // eight lanes hold a block of 32 hidden values
-            const float f[4] = {gelu_exact(v.x), gelu_exact(v.y), gelu_exact(v.z), gelu_exact(v.w)};
-            uint32_t top = __float_as_uint(max_abs_nan(max_abs_nan(max_abs_nan(fabsf(f[0]), f[1]), f[2]), f[3]));
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const bool in = i < m_valid && col < p.N;
-            const uint32_t c = in ? scale_byte(top) : kUnitScale;
-            if (in) {
-                const float g[8] = {f[0], f[1], f[2], f[3], 0.f, 0.f, 0.f, 0.f};
-                const uint32_t q = c == 255u ? 0u : pack_e2m1(g, inverse_scale(c));
-                *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.out) + r * (p.N / 2) + col / 2) = static_cast<uint16_t>(q);
+        __syncwarp();
+        if (rows > 0) ok = mbar_wait(inbox_full, 0, wc) && ok;
+        ok = __syncthreads_and(ok);
+        cluster_arrive();  // every share sent to this CTA is here
+    }
+    const int32_t col = nt * kNTile + lane * 4;
+    // The CTA's rows over its warps; a lane takes four columns.  A quantised output's scale tile is
+    // written whole: the last split also takes the rows past M.  (Kept as tight loops: code that runs
+    // once per launch costs its instruction fetches.  Unrolled over rows and splits this part took
+    // 7000 cycles, so 1000.)
+    const int32_t last = kOut == kOutGeluMx4 && split == splits - 1 ? kMTile : row0 + rows;
+    if (ok) {
+#pragma unroll 1
+        for (int32_t i = row0 + warp; i < last; i += kMx4Threads / 32) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < row0 + rows) {
+                const float* own = tile_f + i * kTilePitch + lane * 4;
+                const float* sent = inbox + (i - row0) * kTilePitch + lane * 4;
+#pragma unroll 1
+                for (int q = 0; q < splits; ++q) {
+                    const float4 w = *reinterpret_cast<const float4*>(q == split ? own : sent);
+                    if (q != split) sent += rows * kTilePitch;
+                    v.x += w.x;
+                    v.y += w.y;
+                    v.z += w.z;
+                    v.w += w.w;
+                }
             }
-            uint32_t word = c << (8 * (lane >> 3));
-            word |= __shfl_xor_sync(0xffffffffu, word, 8);
-            word |= __shfl_xor_sync(0xffffffffu, word, 16);
-            if (lane == 0)
-                *reinterpret_cast<uint32_t*>(p.out_scales + (static_cast<int64_t>(mt) * p.n_tiles + nt) * 512 + (i % 32) * 16 + (i / 32) * 4) = word;
+            const int64_t r = static_cast<int64_t>(mt) * kMTile + i;
+            if (kOut == kOutF32) {
+                if (col < p.N) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + r * p.N + col) = v;
+            } else if (kOut == kOutBf16) {
+                if (col < p.N)
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + r * p.N + col) =
+                        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            } else {
+                // eight lanes hold a block of 32 hidden values
+                const float f[4] = {gelu_exact(v.x), gelu_exact(v.y), gelu_exact(v.z), gelu_exact(v.w)};
+                uint32_t top = __float_as_uint(max_abs_nan(max_abs_nan(max_abs_nan(fabsf(f[0]), f[1]), f[2]), f[3]));
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const bool in = i < m_valid && col < p.N;
+                const uint32_t c = in ? scale_byte(top) : kUnitScale;
+                if (in) {
+                    const float g[8] = {f[0], f[1], f[2], f[3], 0.f, 0.f, 0.f, 0.f};
+                    const uint32_t q = c == 255u ? 0u : pack_e2m1(g, inverse_scale(c));
+                    *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.out) + r * (p.N / 2) + col / 2) = static_cast<uint16_t>(q);
+                }
+                uint32_t word = c << (8 * (lane >> 3));
+                word |= __shfl_xor_sync(0xffffffffu, word, 8);
+                word |= __shfl_xor_sync(0xffffffffu, word, 16);
+                if (lane == 0)
+                    *reinterpret_cast<uint32_t*>(p.out_scales + (static_cast<int64_t>(mt) * p.n_tiles + nt) * 512 + (i % 32) * 16 + (i / 32) * 4) = word;
+            }
         }
     }
-    if (splits > 1) cluster_sync();  // no CTA leaves while another reads its tile
     tcgen05_before_sync();
     __syncthreads();
+    if (splits > 1) cluster_wait();  // this CTA's shares have arrived: none is still read from its tile
     tcgen05_after_sync();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -488,27 +569,6 @@ __device__ __forceinline__ void umma_mx4_pair(uint32_t d, uint64_t a, uint64_t b
 __device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint64_t d) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
-__device__ __forceinline__ void tmem_ld_32x32b_x32_nowait(uint32_t taddr, uint32_t* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(taddr));
-}
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r != 0;
-}
 // Barrier of one epilogue group (128 threads) that also ORs a flag over it: one exit decision.
 __device__ __forceinline__ bool group_sync_or(int group, bool flag) {
     uint32_t r;
@@ -555,15 +615,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         wc->limit = p.wait_limit;
         fence_barrier_init();
     }
+    __syncthreads();
+    cluster_arrive();
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    tcgen05_before_sync();
-    __syncthreads();
-    cluster_sync();  // barriers of both CTAs initialised before any remote arrival
-    tcgen05_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    cluster_wait();  // barriers of both CTAs initialised before any remote arrival
+    if (warp != 0) {  // the copies start at once; the other warps meet when the tensor memory is there
+        tcgen05_before_sync();
+        asm volatile("bar.sync 3, %0;" ::"n"(kPairThreads - 32) : "memory");
+        tcgen05_after_sync();
+    }
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
     if (warp == 0 && lane == 0) {
         // ---------------------------------------------------------------- producer (both CTAs)
@@ -744,7 +808,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 uint32_t v[kCols];
 #pragma unroll
                 for (int c = 0; c < kCols; c += 32) tmem_ld_32x32b_x32_nowait(acc + c, v + c);
-                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                tmem_ld_wait();
                 tcgen05_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(leader_empty + b * 8);
@@ -884,13 +948,25 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
 }
 
 cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
+    // Which kernel, from sizes alone (measured in us, us a product, K = 2048 unless said):
+    //  * up to 128 rows half of a pair's tile would be empty: single CTAs, K split;
+    //  * more 256 x 128 tiles than pairs: 256 x 256 tiles (96 tiles: 9.0, with 128 columns 10.2, single
+    //    CTAs 14.7) - but 256 x 128 where the epilogue is the longer part (gelu on 4096 x 4096 x 1024:
+    //    block 35.5, with 256 columns 39.7);
+    //  * fewer: 256 x 128 tiles (64 tiles: 7.4, single CTAs 8.2; 8 tiles: 7.0 and 6.9), unless splitting K
+    //    makes up for it, which takes K > 2048 (32 tiles at K = 8192: 14.9, split in two 12.5).
     const int64_t pairs = static_cast<int64_t>((q.M + 255) / 256) * ((q.N + 127) / 128);
-    if (2 * pairs >= num_sms()) {
-        static const int force = getenv("MX4N") ? atoi(getenv("MX4N")) : 0;
-        const bool wide = force ? force == 256 : q.out_kind != kMx4OutGelu;
+    const int64_t singles = static_cast<int64_t>((q.M + kMTile - 1) / kMTile) * ((q.N + kNTile - 1) / kNTile);
+    const int32_t k_blocks = (q.K + kKStage - 1) / kKStage;
+    // single CTAs: split K while the clusters fit one wave and every split keeps a block.  (Clusters of
+    // eight are placed two to a GPC at most: 200 x 1000 x 4096 took 10.8 us split in eight, 7.5 in four.)
+    int splits = 1;
+    while (splits < 4 && 2 * splits * singles <= num_sms() && 2 * splits <= k_blocks) splits *= 2;
+    if (q.M > 128 && (splits == 1 || k_blocks <= 8)) {
+        const bool wide = 2 * pairs > num_sms();
         if (q.out_kind == kMx4OutF32) return wide ? launch_pair<kOutF32, 256>(q, st) : launch_pair<kOutF32, 128>(q, st);
         if (q.out_kind == kMx4OutBf16) return wide ? launch_pair<kOutBf16, 256>(q, st) : launch_pair<kOutBf16, 128>(q, st);
-        return wide ? launch_pair<kOutGeluMx4, 256>(q, st) : launch_pair<kOutGeluMx4, 128>(q, st);
+        return launch_pair<kOutGeluMx4, 128>(q, st);
     }
     Mx4Kernel kp;
     std::memset(&kp, 0, sizeof(kp));
@@ -907,13 +983,9 @@ cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
     kp.K = q.K;
     kp.n_tiles = (q.N + kNTile - 1) / kNTile;
     kp.k_tiles = (q.K + 127) / 128;
-    kp.k_blocks = (q.K + kKStage - 1) / kKStage;
+    kp.k_blocks = k_blocks;
     kp.wait_limit = kWaitLimitCycles;
-    const int64_t tiles = static_cast<int64_t>((q.M + kMTile - 1) / kMTile) * kp.n_tiles;
-    // split K while the clusters fit one wave and every split keeps a block
-    int splits = 1;
-    while (splits < 8 && 2 * splits * tiles <= num_sms() && 2 * splits <= kp.k_blocks) splits *= 2;
-    const int64_t grid = tiles * splits;
+    const int64_t grid = singles * splits;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (q.out_kind == kMx4OutF32) return launch_product<kOutF32>(kp, static_cast<int>(grid), splits, q.dependent != 0, st);
     if (q.out_kind == kMx4OutBf16) return launch_product<kOutBf16>(kp, static_cast<int>(grid), splits, q.dependent != 0, st);
