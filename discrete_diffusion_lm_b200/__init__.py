@@ -641,6 +641,7 @@ def _wrong_device(t: torch.Tensor, name: str):
 # (3 us of a call that costs the GPU as little).
 _current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def _device_of(t: torch.Tensor, name: str) -> int:
@@ -673,7 +674,7 @@ def dg_block_norm(x: torch.Tensor, w_pre: Optional[torch.Tensor] = None, *, y: O
     backward pass takes.  x, y: [B*C, d]; gate: [B, d], one row per canvas of C rows.  Pass `out` to
     reuse buffers; out["x"] may be x itself."""
     dev = _device_of(x, "x")
-    if stream is not None or dev != torch.cuda.current_device():
+    if stream is not None or dev != _current_device():
         with _On(dev, stream):
             return dg_block_norm(x, w_pre, y=y, w_post=w_post, gate=gate, C=C, res_scale=res_scale, eps=eps, out=out)
     dtype, shape = x.dtype, x.shape
@@ -696,7 +697,7 @@ def dg_block_norm(x: torch.Tensor, w_pre: Optional[torch.Tensor] = None, *, y: O
         if t is not None:
             p = _arg(t, key, dev, dt, shp)
         else:
-            t = torch.empty_like(x, memory_format=torch.contiguous_format) if shp is shape else torch.empty(shp, dtype=dt, device=device)
+            t = torch.empty_like(x, memory_format=torch.contiguous_format) if shp is shape else torch.empty(*shp, dtype=dt, device=device)
             p = t.data_ptr()
         res[key] = t
         return p
@@ -734,7 +735,7 @@ def dg_block_norm_backward(dx_out: Optional[torch.Tensor], dh: Optional[torch.Te
     the call had them, "dw_pre" (w_pre), "dy", "dw_post" (y) and "dgate" (gate); the parameters'
     gradients are float32."""
     dev = _device_of(x, "x")
-    if stream is not None or dev != torch.cuda.current_device():
+    if stream is not None or dev != _current_device():
         with _On(dev, stream):
             return dg_block_norm_backward(dx_out, dh, x, w_pre, rstd_x=rstd_x, y=y, w_post=w_post, gate=gate,
                                           rstd_y=rstd_y, C=C, res_scale=res_scale, out=out, ws=ws)
@@ -757,7 +758,7 @@ def dg_block_norm_backward(dx_out: Optional[torch.Tensor], dh: Optional[torch.Te
         if t is not None:
             p = _arg(t, key, dev, dt, shp)
         else:
-            t = torch.empty_like(x, memory_format=torch.contiguous_format) if shp is shape else torch.empty(shp, dtype=dt, device=device)
+            t = torch.empty_like(x, memory_format=torch.contiguous_format) if shp is shape else torch.empty(*shp, dtype=dt, device=device)
             p = t.data_ptr()
         res[key] = t
         return p
@@ -810,7 +811,7 @@ def dg_mx4_quantize(x: torch.Tensor, *, out=None, stream=None):
     """x [rows, K] (float32 or bfloat16) in MXFP4: (codes uint8 [rows, K/2], scales uint8 in the shape of
     dg_mx4_scale_shape).  Pass out=(codes, scales) to reuse buffers."""
     dev = _device_of(x, "x")
-    if stream is not None or dev != torch.cuda.current_device():
+    if stream is not None or dev != _current_device():
         with _On(dev, stream):
             return dg_mx4_quantize(x, out=out)
     shape = x.shape
@@ -821,11 +822,12 @@ def dg_mx4_quantize(x: torch.Tensor, *, out=None, stream=None):
     px, ld = _rows_arg(x, "x", dev, x.dtype, shape)
     u8, scale_shape = torch.uint8, dg_mx4_scale_shape(R, K)
     if out is None:
-        codes, scales = torch.empty((R, K // 2), dtype=u8, device=x.device), torch.empty(scale_shape, dtype=u8, device=x.device)
+        codes, scales = torch.empty(R, K // 2, dtype=u8, device=x.device), torch.empty(*scale_shape, dtype=u8, device=x.device)
+        pc, ps = codes.data_ptr(), scales.data_ptr()
     else:
         codes, scales = out
-    rc = lib().dg_mx4_quantize(px, dt, ld, R, K, _arg(codes, "codes", dev, u8, (R, K // 2)),
-                               _arg(scales, "scales", dev, u8, scale_shape), _current_stream(dev))
+        pc, ps = _arg(codes, "codes", dev, u8, (R, K // 2)), _arg(scales, "scales", dev, u8, scale_shape)
+    rc = lib().dg_mx4_quantize(px, dt, ld, R, K, pc, ps, _current_stream(dev))
     if rc:
         _check("dg_mx4_quantize", rc)
     return codes, scales
@@ -835,18 +837,23 @@ def dg_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, *, dtype: torch
                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values [rows, K] that MXFP4 codes and scales stand for."""
     dev = _device_of(codes, "codes")
-    if stream is not None or dev != torch.cuda.current_device():
+    if stream is not None or dev != _current_device():
         with _On(dev, stream):
             return dg_mx4_dequantize(codes, scales, dtype=dtype, out=out)
     if len(codes.shape) != 2:
         raise ValueError("codes must be a 2-D tensor")
     R, K = codes.shape[0], 2 * codes.shape[1]
     u8 = torch.uint8
+    dt = _DTYPE.get(dtype)
+    if dt is None:
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
     if out is None:
-        out = torch.empty((R, K), dtype=dtype, device=codes.device)
+        out = torch.empty(R, K, dtype=dtype, device=codes.device)
+        po = out.data_ptr()
+    else:
+        po = _arg(out, "out", dev, dtype, (R, K))
     rc = lib().dg_mx4_dequantize(_arg(codes, "codes", dev, u8, codes.shape), _arg(scales, "scales", dev, u8, dg_mx4_scale_shape(R, K)),
-                                 R, K, _arg(out, "out", dev, dtype, (R, K)), _dtype_of(out, "out"),
-                                 _current_stream(dev))
+                                 R, K, po, dt, _current_stream(dev))
     if rc:
         _check("dg_mx4_dequantize", rc)
     return out
@@ -861,19 +868,25 @@ def _mx4_arg(q, name: str, dev: int, rows: int, K: int):
 def dg_mx4_matmul(a, w, *, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     """a w^T [M, N] of two MXFP4 matrices a = (codes, scales) [M, K] and w [N, K], fp32 accumulation."""
-    dev = _device_of(a[0], "a codes")
-    if stream is not None or dev != torch.cuda.current_device():
+    (ac, asc), (wc, wsc) = a, w
+    dev = _device_of(ac, "a codes")
+    if stream is not None or dev != _current_device():
         with _On(dev, stream):
             return dg_mx4_matmul(a, w, dtype=dtype, out=out)
-    if len(a[0].shape) != 2 or len(w[0].shape) != 2:
+    if ac.dim() != 2 or wc.dim() != 2:
         raise ValueError("codes must be 2-D tensors")
-    M, K, N = a[0].shape[0], 2 * a[0].shape[1], w[0].shape[0]
+    (M, half), N, u8, dt = ac.shape, wc.shape[0], torch.uint8, _DTYPE.get(dtype)
+    if dt is None:
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=a[0].device)
-    pa, psa = _mx4_arg(a, "a", dev, M, K)
-    pw, psw = _mx4_arg(w, "w", dev, N, K)
-    rc = lib().dg_mx4_matmul(pa, psa, pw, psw, M, N, K, _arg(out, "out", dev, dtype, (M, N)), _dtype_of(out, "out"),
-                             _current_stream(dev))
+        out = torch.empty(M, N, dtype=dtype, device=ac.device)
+        po = out.data_ptr()
+    else:
+        po = _arg(out, "out", dev, dtype, (M, N))
+    K = 2 * half
+    rc = lib().dg_mx4_matmul(_arg(ac, "a codes", dev, u8, (M, half)), _arg(asc, "a scales", dev, u8, dg_mx4_scale_shape(M, K)),
+                             _arg(wc, "w codes", dev, u8, (N, half)), _arg(wsc, "w scales", dev, u8, dg_mx4_scale_shape(N, K)),
+                             M, N, K, po, dt, _current_stream(dev))
     if rc:
         _check("dg_mx4_matmul", rc)
     return out
@@ -885,7 +898,7 @@ def dg_ffw_mx4(z: torch.Tensor, w1, w2, *, out: Optional[torch.Tensor] = None, w
     scales) of W1 transposed, [d_ff, d]; w2 of W2 transposed, [d, d_ff]: for weights as dg_ffw takes them,
     dg_mx4_quantize(W.t().contiguous())."""
     dev = _device_of(z, "z")
-    if stream is not None or dev != torch.cuda.current_device():
+    if stream is not None or dev != _current_device():
         with _On(dev, stream):
             return dg_ffw_mx4(z, w1, w2, out=out, ws=ws)
     if len(z.shape) != 2:
@@ -897,13 +910,16 @@ def dg_ffw_mx4(z: torch.Tensor, w1, w2, *, out: Optional[torch.Tensor] = None, w
     p1, ps1 = _mx4_arg(w1, "w1", dev, dff, d)
     p2, ps2 = _mx4_arg(w2, "w2", dev, d, dff)
     if out is None:
-        out = torch.empty((R, d), dtype=bf16, device=z.device)
+        out = torch.empty_like(z)
+        po = out.data_ptr()
+    else:
+        po = _arg(out, "out", dev, bf16, (R, d))
     L = lib()
     if ws is None:
         ws = torch.empty(max(256, L.dg_ffw_mx4_workspace_size(R, d, dff)), dtype=torch.uint8, device=z.device)
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous tensor on the device of z")
-    rc = L.dg_ffw_mx4(pz, R, d, dff, p1, ps1, p2, ps2, _arg(out, "out", dev, bf16, (R, d)), ws.data_ptr(),
+    rc = L.dg_ffw_mx4(pz, R, d, dff, p1, ps1, p2, ps2, po, ws.data_ptr(),
                       ws.numel() * ws.element_size(), _current_stream(dev))
     if rc:
         _check("dg_ffw_mx4", rc)
