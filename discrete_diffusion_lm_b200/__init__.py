@@ -112,7 +112,7 @@ def lib() -> ctypes.CDLL:
                                                _sz, _p]
         L.dg_block_norm.argtypes = [_p, _i64, _p, _i64, _int, _p, _p, _p, _int, _i32, _i32, _i32, _f32, _f32, _p, _p,
                                     _p, _p, _p]
-        L.dg_block_norm_backward_workspace_size.argtypes = [_i32, _i32, _i32, _int]
+        L.dg_block_norm_backward_workspace_size.argtypes = [_i32, _i32, _i32, _int, _int]
         L.dg_block_norm_backward_workspace_size.restype = _sz
         L.dg_block_norm_backward.argtypes = [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _int, _p, _p, _p, _int, _i32,
                                              _i32, _i32, _f32, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]
@@ -789,7 +789,7 @@ def dg_block_norm_backward(dx_out: Optional[torch.Tensor], dh: Optional[torch.Te
     elif w_post is not None or gate is not None:
         raise ValueError("w_post and gate come only with y")
     L = lib()
-    nbytes = L.dg_block_norm_backward_workspace_size(R // C, C, d, pg is not None)
+    nbytes = L.dg_block_norm_backward_workspace_size(R // C, C, d, act, pg is not None)
     if ws is None:
         ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=x.device)
     elif ws.get_device() != dev or not ws.is_contiguous():

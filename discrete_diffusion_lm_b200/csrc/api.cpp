@@ -200,11 +200,11 @@ int check_norm_rows(const char* name, const void* p, int64_t ld, int dtype, int3
 struct NormRuns {
     int32_t B, C, runs, run_rows;
 };
-NormRuns norm_runs(int32_t B, int32_t C, bool have_gate) {
+NormRuns norm_runs(int32_t B, int32_t C, int32_t d, int act_dtype, bool have_gate) {
     NormRuns n;
     n.B = have_gate ? B : 1;
     n.C = have_gate ? C : B * C;
-    const int32_t want = block_norm_runs(n.B, n.C);
+    const int32_t want = block_norm_runs(n.B, n.C, d, act_dtype == DG_BF16);
     n.run_rows = (n.C + want - 1) / want;
     n.runs = (n.C + n.run_rows - 1) / n.run_rows;
     return n;
@@ -255,15 +255,16 @@ int dg_device_error(int* code) {
     if ((rc = check_device()) != DG_OK) return rc;
     const cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-    int c[5] = {0, 0, 0, 0, 0};
+    int c[6] = {0, 0, 0, 0, 0, 0};
     cudaError_t r = read_and_clear_device_error(&c[0]);
     if (r == cudaSuccess) r = read_and_clear_pass_error(&c[1]);
     if (r == cudaSuccess) r = read_and_clear_ops_error(&c[2]);
     if (r == cudaSuccess) r = read_and_clear_noise_error(&c[3]);
     if (r == cudaSuccess) r = read_and_clear_mx4_error(&c[4]);
+    if (r == cudaSuccess) r = read_and_clear_norm_error(&c[5]);
     if (r != cudaSuccess) return cuda_fail(r, "reading the device error words");
     *code = 0;
-    for (int k = 0; k < 5; ++k)  // the largest code: a failed check (2) before an expired wait (1)
+    for (int k = 0; k < 6; ++k)  // the largest code: a failed check (2) before an expired wait (1)
         if (c[k] > *code) *code = c[k];
     return DG_OK;
 }
@@ -856,9 +857,9 @@ int dg_block_norm(const void* x, int64_t ld_x, const void* y, int64_t ld_y, int 
     return DG_OK;
 }
 
-size_t dg_block_norm_backward_workspace_size(int32_t B, int32_t C, int32_t d, int have_gate) {
-    if (B < 1 || C < 1 || d < 1 || static_cast<long long>(B) * C > 0x7fffffffLL) return 0;
-    const NormRuns n = norm_runs(B, C, have_gate != 0);
+size_t dg_block_norm_backward_workspace_size(int32_t B, int32_t C, int32_t d, int act_dtype, int have_gate) {
+    if (B < 1 || C < 1 || d < 8 || !valid_dtype(act_dtype) || static_cast<long long>(B) * C > 0x7fffffffLL) return 0;
+    const NormRuns n = norm_runs(B, C, d, act_dtype, have_gate != 0);
     return 2 * static_cast<size_t>(n.B) * n.runs * d * sizeof(float);
 }
 
@@ -889,14 +890,14 @@ int dg_block_norm_backward(const void* dx_out, int64_t ld_dx_out, const void* dh
     for (const void* q : in)
         if (q && (q == dx || q == dy)) return fail(DG_ERR_INVALID_ARG, "dx and dy may not alias an input");
     if (dx == dy) return fail(DG_ERR_INVALID_ARG, "dx and dy may not alias");
-    const size_t need = dg_block_norm_backward_workspace_size(B, C, d, gate != nullptr);
+    const size_t need = dg_block_norm_backward_workspace_size(B, C, d, act_dtype, gate != nullptr);
     if (!workspace || workspace_bytes < need)
         return fail(DG_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, need);
     if (!aligned16(workspace)) return fail(DG_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
     if ((rc = check_device()) != DG_OK) return rc;
     BlockNormBackwardParams p;
     std::memset(&p, 0, sizeof(p));
-    const NormRuns n = norm_runs(B, C, gate != nullptr);
+    const NormRuns n = norm_runs(B, C, d, act_dtype, gate != nullptr);
     p.dx_out = dx_out;
     p.dh = dh;
     p.x = x;

@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "kernels.cuh"
+#include "tensor_core.cuh"
 
 namespace dg {
 
@@ -207,6 +208,319 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) block_norm_ke
     }
 }
 
+// ------------------------------------------------------------------------------------ rows in a ring
+// With many rows a group of kW warps walks a run of them, the next rows' bulk copies in flight in a
+// ring of shared-memory slots with a barrier each.  Beside memory it is instructions that bound such a
+// walk, so the parameters stay in registers, as fp32 pairs for the packed fma.rn.f32x2, and widths
+// that fill every thread's vectors (kFull) have no column checks.  A CTA has kGroups groups, each with
+// its own ring and named barrier.
+using Pair = unsigned long long;  // two fp32 values
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ void unpair(Pair p, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float sum2(Pair p) {
+    float a, b;
+    unpair(p, a, b);
+    return a + b;
+}
+template <typename T, int kP>
+__device__ __forceinline__ void unpack_pairs(const uint4& v, Pair (&p)[kP]) {
+    float f[2 * kP];
+    Vec<T>::unpack(v, f);
+#pragma unroll
+    for (int i = 0; i < kP; ++i) p[i] = pair(f[2 * i], f[2 * i + 1]);
+}
+template <typename T, int kP>
+__device__ __forceinline__ uint4 pack_pairs(const Pair (&p)[kP]) {
+    float f[2 * kP];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) unpair(p[i], f[2 * i], f[2 * i + 1]);
+    return Vec<T>::pack(f);
+}
+template <typename P, int kP>
+__device__ __forceinline__ void load_pairs(const P* src, Pair (&p)[kP]) {
+    float f[2 * kP];
+    load_params<2 * kP>(src, f);
+#pragma unroll
+    for (int i = 0; i < kP; ++i) p[i] = pair(f[2 * i], f[2 * i + 1]);
+}
+
+// 1 / sqrt(x): the hardware's approximation and one Newton step (error about 2^-23).
+__device__ __forceinline__ float rsqrt_newton(float x) {
+    const float r = rsqrtf(x);
+    return r * fmaf(-0.5f * x * r, r, 1.5f);
+}
+
+constexpr int kMaxSlots = 8;
+constexpr int kNormCtas = 2;  // per SM, of the backward pass
+template <int kGroups>
+struct Rings {
+    uint64_t full[kGroups][kMaxSlots];
+    WaitCtl wc;
+};
+template <int kGroups>
+__device__ __forceinline__ void rings_init(Rings<kGroups>& rings) {
+    if (threadIdx.x == 0) {
+        for (int g = 0; g < kGroups; ++g)
+            for (int s = 0; s < kMaxSlots; ++s) mbar_init(&rings.full[g][s], 1);
+        rings.wc.abort = 0;
+        rings.wc.limit = kWaitLimitCycles;
+        fence_barrier_init();
+    }
+    __syncthreads();
+}
+// A row that never arrives: the error is recorded and the walk goes on (its waits end at once), so
+// that every thread keeps to the same barriers.  Copies still in flight are waited for at the end.
+template <int kGroups>
+__device__ __forceinline__ void rings_drain(Rings<kGroups>& rings, int group, bool leader, int rows, int slots) {
+    if (leader && aborted(&rings.wc)) {
+        const long long t0 = clock64();
+        for (int i = max(0, rows - slots); i < rows; ++i)
+            while (!mbar_try_wait(&rings.full[group][i % slots], (i / slots) & 1) && clock64() - t0 < rings.wc.limit) {
+            }
+    }
+    __syncthreads();
+}
+// Barrier of a group of kW warps.
+template <int kW>
+__device__ __forceinline__ void group_barrier(int group) {
+    if (kW == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * kW) : "memory");
+}
+// kV sums over the group's threads, every thread receiving all of them; `sh`: kV * kW floats, not
+// reused before the group's next barrier.  Every thread has passed a group barrier (kW > 1).
+template <int kW, int kV>
+__device__ __forceinline__ void group_sums(float (&v)[kV], float* sh, int group) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v[i] = warp_sum(v[i]);
+    if (kW == 1) return;
+    const int w = (threadIdx.x >> 5) % kW;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) sh[i * kW + w] = v[i];
+    }
+    group_barrier<kW>(group);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+        if (kW % 4 == 0) {
+            v[i] = 0.f;
+#pragma unroll
+            for (int q = 0; q < kW; q += 4) {
+                const float4 w4 = *reinterpret_cast<const float4*>(sh + i * kW + q);
+                v[i] += (w4.x + w4.y) + (w4.z + w4.w);
+            }
+        } else {
+            v[i] = sh[i * kW];
+#pragma unroll
+            for (int q = 1; q < kW; ++q) v[i] += sh[i * kW + q];
+        }
+    }
+}
+// row_rstd for a group (see there), of values held as pairs or as raw vectors.
+template <typename T, int kP>
+__device__ __forceinline__ void as_pairs(const Pair (&f)[kP], Pair (&p)[kP]) {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) p[i] = f[i];
+}
+template <typename T, int kP>
+__device__ __forceinline__ void as_pairs(const uint4& v, Pair (&p)[kP]) {
+    unpack_pairs<T>(v, p);
+}
+template <typename T, int kW, int kNV, typename V>
+__device__ __forceinline__ float group_rstd(const V (&v)[kNV], float inv_d, float eps, float* sh, double* sh64, int group) {
+    constexpr int kP = Vec<T>::kN / 2;
+    Pair two[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < kNV; ++k) {
+        Pair f[kP];
+        as_pairs<T>(v[k], f);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) two[i & 1] = fma2(f[i], f[i], two[i & 1]);
+    }
+    float s[1] = {sum2(two[0]) + sum2(two[1])};
+    group_sums<kW>(s, sh, group);
+    const float ms = fmaf(s[0], inv_d, eps);
+    if (ms > 1e-30f && ms < INFINITY) return rsqrt_newton(ms);
+    double a = 0.0;
+#pragma unroll
+    for (int k = 0; k < kNV; ++k) {
+        Pair f[kP];
+        as_pairs<T>(v[k], f);
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            float lo, hi;
+            unpair(f[i], lo, hi);
+            a = fma(static_cast<double>(lo), static_cast<double>(lo), fma(static_cast<double>(hi), static_cast<double>(hi), a));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (kW > 1) {
+        group_barrier<kW>(group);
+        if ((threadIdx.x & 31) == 0) sh64[(threadIdx.x >> 5) % kW] = a;
+        group_barrier<kW>(group);
+        a = 0.0;
+        for (int w = 0; w < kW; ++w) a += sh64[w];
+    }
+    return static_cast<float>(1.0 / sqrt(fma(a, static_cast<double>(inv_d), static_cast<double>(eps))));
+}
+
+template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas, bool kFull>
+__global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
+    block_norm_rows_kernel(const __grid_constant__ BlockNormParams p, int slots, int run) {
+    constexpr int kN = Vec<T>::kN, kP = kN / 2, kThreads = 32 * kW;
+    extern __shared__ __align__(128) uint8_t slots_mem[];
+    __shared__ Rings<kGroups> rings;
+    __shared__ __align__(16) float sh[kGroups][2][kW];
+    __shared__ double sh64[kGroups][kW];
+    const int group = threadIdx.x / kThreads, t = threadIdx.x % kThreads;
+    const int n_vec = kFull ? kNV * kThreads : p.d / kN, d = kFull ? kNV * kThreads * kN : p.d;
+    const bool pre = p.w_pre != nullptr, post = p.y != nullptr;
+    const uint32_t row_bytes = static_cast<uint32_t>(d) * sizeof(T), slot_bytes = row_bytes * (post ? 2 : 1);
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * kGroups + group) * run;
+    const int r0 = static_cast<int>(min(first, static_cast<int64_t>(p.R))), n = min(run, p.R - r0);
+    const float inv_d = 1.0f / static_cast<float>(d);
+    uint8_t* ring = slots_mem + group * slots * slot_bytes;
+    rings_init(rings);
+    const T* next_x = static_cast<const T*>(p.x) + static_cast<int64_t>(r0) * p.ld_x;
+    const T* next_y = static_cast<const T*>(p.y) + static_cast<int64_t>(r0) * p.ld_y;
+    const auto fetch = [&](int slot) {  // the next row, into a free slot
+        uint64_t* bar = &rings.full[group][slot];
+        uint8_t* dst = ring + slot * slot_bytes;
+        mbar_arrive_expect_tx(bar, slot_bytes);
+        bulk_load(dst, next_x, row_bytes, bar);
+        if (post) bulk_load(dst + row_bytes, next_y, row_bytes, bar);
+        next_x += p.ld_x;
+        next_y += p.ld_y;
+    };
+    if (t == 0)
+        for (int i = 0; i < min(n, slots); ++i) fetch(i);
+    Pair wc[kNV][kP], wpre[kNV][kP];  // res_scale gate w_post, w_pre
+    int canvas = r0 / p.C, left = 0;  // rows before wc is of the next canvas
+    const auto load_post = [&]() {
+        const Pair scale = pair(p.res_scale, p.res_scale);
+#pragma unroll
+        for (int k = 0; k < kNV; ++k) {
+            const int c = t + k * kThreads;
+            if (kFull || c < n_vec) {
+                load_pairs(static_cast<const P*>(p.w_post) + c * kN, wc[k]);
+                if (p.gate) {
+                    Pair g[kP];
+                    load_pairs(static_cast<const P*>(p.gate) + static_cast<int64_t>(canvas) * d + c * kN, g);
+#pragma unroll
+                    for (int j = 0; j < kP; ++j) wc[k][j] = mul2(wc[k][j], g[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < kP; ++j) wc[k][j] = mul2(wc[k][j], scale);
+            }
+        }
+    };
+    if (post) load_post();
+    left = p.gate ? p.C - r0 % p.C : 0x7fffffff;
+#pragma unroll
+    for (int k = 0; k < kNV; ++k) {
+        const int c = t + k * kThreads;
+        if (pre && (kFull || c < n_vec)) load_pairs(static_cast<const P*>(p.w_pre) + c * kN, wpre[k]);
+    }
+    T* xo = static_cast<T*>(p.x_out) + static_cast<int64_t>(r0) * d + t * kN;
+    T* h = static_cast<T*>(p.h) + static_cast<int64_t>(r0) * d + t * kN;
+    const uint8_t* src0 = ring + t * 16;
+    int slot = 0, phase = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i, --left, xo += d, h += d) {
+        if (left == 0) {
+            ++canvas;
+            left = p.C;
+            load_post();
+        }
+        mbar_wait(&rings.full[group][slot], phase, &rings.wc);
+        const uint8_t* src = src0 + slot * slot_bytes;
+        Pair fx[kNV][kP], fy[kNV][kP];
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < kNV; ++k) {
+            const bool in = kFull || t + k * kThreads < n_vec;
+            unpack_pairs<T>(in ? *reinterpret_cast<const uint4*>(src + k * (16 * kThreads)) : zero, fx[k]);
+            if (post) unpack_pairs<T>(in ? *reinterpret_cast<const uint4*>(src + row_bytes + k * (16 * kThreads)) : zero, fy[k]);
+        }
+        if (post) {
+            const float rstd = group_rstd<T, kW>(fy, inv_d, p.eps, sh[group][0], sh64[group], group);
+            if (t == 0 && p.rstd_y) p.rstd_y[r0 + i] = rstd;
+            const Pair rstd2 = pair(rstd, rstd);
+#pragma unroll
+            for (int k = 0; k < kNV; ++k) {
+                if (kFull || t + k * kThreads < n_vec) {
+#pragma unroll
+                    for (int j = 0; j < kP; ++j) fx[k][j] = fma2(mul2(fy[k][j], rstd2), wc[k][j], fx[k][j]);
+                    *reinterpret_cast<uint4*>(xo + k * (kN * kThreads)) = pack_pairs<T>(fx[k]);
+                }
+            }
+        }
+        float rstd = 0.f;
+        if (pre) rstd = group_rstd<T, kW>(fx, inv_d, p.eps, sh[group][1], sh64[group], group);
+        // between this barrier and the last row's, the slot and the exchange's floats have been read
+        if (kW == 1 || !post || !pre) group_barrier<kW>(group);
+        if (t == 0 && i + slots < n) fetch(slot);
+        if (pre) {
+            if (t == 0 && p.rstd_x) p.rstd_x[r0 + i] = rstd;
+            const Pair rstd2 = pair(rstd, rstd);
+#pragma unroll
+            for (int k = 0; k < kNV; ++k) {
+                if (kFull || t + k * kThreads < n_vec) {
+#pragma unroll
+                    for (int j = 0; j < kP; ++j) fx[k][j] = mul2(mul2(fx[k][j], rstd2), wpre[k][j]);
+                    *reinterpret_cast<uint4*>(h + k * (kN * kThreads)) = pack_pairs<T>(fx[k]);
+                }
+            }
+        }
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    rings_drain(rings, group, t == 0, n, slots);
+}
+
+// kCtas CTAs per SM share its shared memory.
+template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas, bool kFull>
+cudaError_t launch_rows_as(const BlockNormParams& p, cudaStream_t st) {
+    constexpr int kRingBytes = 200 * 1024 / kCtas;
+    const int slot = p.d * static_cast<int>(sizeof(T)) * (p.y ? 2 : 1);
+    const int slots = std::min(kMaxSlots, kRingBytes / (slot * kGroups));
+    const int64_t groups = static_cast<int64_t>(kCtas) * num_sms() * kGroups;
+    const int run = static_cast<int>((p.R + groups - 1) / groups);
+    const int64_t ctas = (p.R + static_cast<int64_t>(run) * kGroups - 1) / (static_cast<int64_t>(run) * kGroups);
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [] {
+        attr_err = cudaFuncSetAttribute(block_norm_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    block_norm_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull><<<static_cast<unsigned>(ctas), 32 * kW * kGroups, kGroups * slots * slot, st>>>(p, slots, run);
+    note_launches(1);
+    return cudaGetLastError();
+}
+template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas>
+cudaError_t launch_rows(const BlockNormParams& p, cudaStream_t st) {
+    if (p.d == kNV * kW * 32 * Vec<T>::kN) return launch_rows_as<T, P, kW, kGroups, kNV, kCtas, true>(p, st);
+    return launch_rows_as<T, P, kW, kGroups, kNV, kCtas, false>(p, st);
+}
+
 template <typename T, typename P, int kWarps, int kNV>
 cudaError_t launch_forward(const BlockNormParams& p, cudaStream_t st) {
     const unsigned grid = static_cast<unsigned>(kWarps == 1 ? (static_cast<int64_t>(p.R) + 3) / 4 : p.R);
@@ -218,6 +532,14 @@ cudaError_t launch_forward(const BlockNormParams& p, cudaStream_t st) {
 template <typename T, typename P>
 cudaError_t forward_by_width(const BlockNormParams& p, cudaStream_t st) {
     const int n_vec = p.d / Vec<T>::kN;
+    if (p.R >= 8 * num_sms() && n_vec <= 1024) {
+        if (n_vec <= 32) return launch_rows<T, P, 1, 8, 1, 3>(p, st);
+        if (n_vec <= 64) return launch_rows<T, P, 1, 8, 2, 2>(p, st);
+        if (n_vec <= 128) return launch_rows<T, P, 2, 4, 2, 2>(p, st);
+        if (n_vec <= 256) return launch_rows<T, P, 4, 2, 2, 2>(p, st);
+        if (n_vec <= 512) return launch_rows<T, P, 8, 1, 2, 2>(p, st);
+        return launch_rows<T, P, 16, 1, 2, 1>(p, st);
+    }
     if (n_vec <= 32) return launch_forward<T, P, 1, 1>(p, st);
     if (n_vec <= 64) return launch_forward<T, P, 1, 2>(p, st);
     if (n_vec <= 128) return launch_forward<T, P, 2, 2>(p, st);
@@ -229,13 +551,18 @@ cudaError_t forward_by_width(const BlockNormParams& p, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------------------ backward
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 // The second mean needs dx, which needs the first; expanding it,
 //   sum c dx v = sum c (dx' + rstd_x t) v - rstd_x mean(t m) sum c m v,
 // so the three sums  sum t m,  sum c (dx' + rstd_x t) v,  sum c m v  take one exchange per row.
-// A CTA walks a run of rows of one canvas and keeps its columns' sums of dh m and dx v in
-// registers; the runs' partial sums go to the workspace and are added in a fixed order.
+// A CTA walks a run of rows of one canvas and keeps its columns' sums of dh m and dx v in registers;
+// the runs' partial sums go to the workspace and are added in a fixed order.
+// This form is for rows too wide for the ring further down: a row is read twice, from memory (the next
+// row is on its way to L2 meanwhile) and then from L1, as registers hold the columns' sums only.
 template <typename T, typename P, int kWarps, int kNV>
-__global__ void __launch_bounds__(32 * kWarps) block_norm_backward_kernel(const __grid_constant__ BlockNormBackwardParams p) {
+__global__ void __launch_bounds__(32 * kWarps, 1) block_norm_backward_kernel(const __grid_constant__ BlockNormBackwardParams p) {
     constexpr int kN = Vec<T>::kN;
     constexpr int kThreads = 32 * kWarps;
     __shared__ float sh[2][3 * kWarps];
@@ -246,7 +573,7 @@ __global__ void __launch_bounds__(32 * kWarps) block_norm_backward_kernel(const 
     const int64_t r1 = min(r0 + p.run_rows, static_cast<int64_t>(b + 1) * p.C);
     const bool pre = p.w_pre != nullptr, post = p.y != nullptr;
     const float inv_d = 1.0f / static_cast<float>(p.d);
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const P* gate = p.gate ? static_cast<const P*>(p.gate) + static_cast<int64_t>(b) * p.d : nullptr;
     float acc_pre[kNV][kN], acc_post[kNV][kN];
 #pragma unroll
     for (int k = 0; k < kNV; ++k)
@@ -254,83 +581,72 @@ __global__ void __launch_bounds__(32 * kWarps) block_norm_backward_kernel(const 
         for (int i = 0; i < kN; ++i) acc_pre[k][i] = acc_post[k][i] = 0.f;
 
     int parity = 0;
+#pragma unroll 1
     for (int64_t r = r0; r < r1; ++r, parity ^= 1) {
-        uint4 gv[kNV], hv[kNV], xv[kNV], yv[kNV];
-#pragma unroll
-        for (int k = 0; k < kNV; ++k) {
-            const int c = t + k * kThreads;
-            const bool in = c < n_vec;
-            gv[k] = in && p.dx_out ? load16(static_cast<const T*>(p.dx_out) + r * p.ld_dx_out + c * kN) : zero;
-            hv[k] = in && pre ? load16(static_cast<const T*>(p.dh) + r * p.ld_dh + c * kN) : zero;
-            xv[k] = in && pre ? load16(static_cast<const T*>(p.x) + r * p.ld_x + c * kN) : zero;
-            yv[k] = in && post ? load16(static_cast<const T*>(p.y) + r * p.ld_y + c * kN) : zero;
+        if (t == 0 && r + 1 < r1) {
+            const uint32_t bytes = static_cast<uint32_t>(p.d) * sizeof(T);
+            if (p.dx_out) prefetch_l2(static_cast<const T*>(p.dx_out) + (r + 1) * p.ld_dx_out, bytes);
+            if (pre) prefetch_l2(static_cast<const T*>(p.dh) + (r + 1) * p.ld_dh, bytes);
+            if (pre) prefetch_l2(static_cast<const T*>(p.x) + (r + 1) * p.ld_x, bytes);
+            if (post) prefetch_l2(static_cast<const T*>(p.y) + (r + 1) * p.ld_y, bytes);
         }
         const float rx = pre ? p.rstd_x[r] : 0.f, ry = post ? p.rstd_y[r] : 0.f;
-        const P* gate = p.gate ? static_cast<const P*>(p.gate) + static_cast<int64_t>(b) * p.d : nullptr;
-        float s[3] = {0.f, 0.f, 0.f};
+        // a vector's columns: the gradients, m, v and t = dh w_pre, c = gate w_post (zero where the call has none)
+        const auto read = [&](int c, float(&g)[kN], float(&h)[kN], float(&m)[kN], float(&v)[kN], float(&tt)[kN], float(&cc)[kN]) {
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            Vec<T>::unpack(p.dx_out ? load16(static_cast<const T*>(p.dx_out) + r * p.ld_dx_out + c * kN) : zero, g);
+            Vec<T>::unpack(pre ? load16(static_cast<const T*>(p.dh) + r * p.ld_dh + c * kN) : zero, h);
+            Vec<T>::unpack(pre ? load16(static_cast<const T*>(p.x) + r * p.ld_x + c * kN) : zero, m);
+            Vec<T>::unpack(post ? load16(static_cast<const T*>(p.y) + r * p.ld_y + c * kN) : zero, v);
+            if (pre) load_params<kN>(static_cast<const P*>(p.w_pre) + c * kN, tt);
+            if (post) load_params<kN>(static_cast<const P*>(p.w_post) + c * kN, cc);
+            if (gate) {
+                float f[kN];
+                load_params<kN>(gate + c * kN, f);
 #pragma unroll
+                for (int i = 0; i < kN; ++i) cc[i] *= f[i];
+            }
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                m[i] *= rx;
+                v[i] *= ry;
+                tt[i] = pre ? tt[i] * h[i] : 0.f;
+                cc[i] = post ? cc[i] * p.res_scale : 0.f;
+            }
+        };
+        float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll 2
         for (int k = 0; k < kNV; ++k) {
             const int c = t + k * kThreads;
             if (c < n_vec) {
-                float fg[kN], fh[kN], fx[kN], fy[kN], wp[kN], wc[kN];
-                Vec<T>::unpack(gv[k], fg);
-                Vec<T>::unpack(hv[k], fh);
-                Vec<T>::unpack(xv[k], fx);
-                Vec<T>::unpack(yv[k], fy);
-                if (pre) load_params<kN>(static_cast<const P*>(p.w_pre) + c * kN, wp);
-                if (post) load_params<kN>(static_cast<const P*>(p.w_post) + c * kN, wc);
-                if (gate) {
-                    float g[kN];
-                    load_params<kN>(gate + c * kN, g);
-#pragma unroll
-                    for (int i = 0; i < kN; ++i) wc[i] *= g[i];
-                }
+                float g[kN], h[kN], m[kN], v[kN], tt[kN], cc[kN];
+                read(c, g, h, m, v, tt, cc);
 #pragma unroll
                 for (int i = 0; i < kN; ++i) {
-                    const float m = fx[i] * rx, tt = pre ? fh[i] * wp[i] : 0.f;
-                    s[0] = fmaf(tt, m, s[0]);
-                    if (post) {
-                        const float cv = wc[i] * (fy[i] * ry);
-                        s[1] = fmaf(cv, fmaf(rx, tt, fg[i]), s[1]);
-                        s[2] = fmaf(cv, m, s[2]);
-                    }
+                    const float cv = cc[i] * v[i];
+                    s[0] = fmaf(tt[i], m[i], s[0]);
+                    s[1] = fmaf(cv, fmaf(rx, tt[i], g[i]), s[1]);
+                    s[2] = fmaf(cv, m[i], s[2]);
                 }
             }
         }
         row_sums<kWarps>(s, sh[parity]);
-        const float m1 = s[0] * inv_d;
-        const float m2 = p.res_scale * fmaf(-rx * m1, s[2], s[1]) * inv_d;
+        const float m1 = s[0] * inv_d, m2 = fmaf(-rx * m1, s[2], s[1]) * inv_d;
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
             const int c = t + k * kThreads;
             if (c < n_vec) {
-                float fg[kN], fh[kN], fx[kN], fy[kN], wp[kN], wc[kN];
-                Vec<T>::unpack(gv[k], fg);
-                Vec<T>::unpack(hv[k], fh);
-                Vec<T>::unpack(xv[k], fx);
-                Vec<T>::unpack(yv[k], fy);
-                if (pre) load_params<kN>(static_cast<const P*>(p.w_pre) + c * kN, wp);
-                if (post) load_params<kN>(static_cast<const P*>(p.w_post) + c * kN, wc);
-                if (gate) {
-                    float g[kN];
-                    load_params<kN>(gate + c * kN, g);
-#pragma unroll
-                    for (int i = 0; i < kN; ++i) wc[i] *= g[i];
-                }
-                float dx[kN], dy[kN];
+                float g[kN], h[kN], m[kN], v[kN], tt[kN], cc[kN];
+                read(c, g, h, m, v, tt, cc);
 #pragma unroll
                 for (int i = 0; i < kN; ++i) {
-                    const float m = fx[i] * rx, tt = pre ? fh[i] * wp[i] : 0.f;
-                    dx[i] = fmaf(rx, fmaf(-m, m1, tt), fg[i]);
-                    acc_pre[k][i] = fmaf(fh[i], m, acc_pre[k][i]);
-                    if (post) {
-                        const float v = fy[i] * ry;
-                        acc_post[k][i] = fmaf(dx[i], v, acc_post[k][i]);
-                        dy[i] = ry * fmaf(-v, m2, p.res_scale * wc[i] * dx[i]);
-                    }
+                    g[i] = fmaf(rx, fmaf(-m[i], m1, tt[i]), g[i]);  // dx
+                    acc_pre[k][i] = fmaf(h[i], m[i], acc_pre[k][i]);
+                    acc_post[k][i] = fmaf(g[i], v[i], acc_post[k][i]);
+                    cc[i] = ry * fmaf(-v[i], m2, cc[i] * g[i]);  // dy
                 }
-                *reinterpret_cast<uint4*>(static_cast<T*>(p.dx) + r * p.d + c * kN) = Vec<T>::pack(dx);
-                if (post) *reinterpret_cast<uint4*>(static_cast<T*>(p.dy) + r * p.d + c * kN) = Vec<T>::pack(dy);
+                *reinterpret_cast<uint4*>(static_cast<T*>(p.dx) + r * p.d + c * kN) = Vec<T>::pack(g);
+                if (post) *reinterpret_cast<uint4*>(static_cast<T*>(p.dy) + r * p.d + c * kN) = Vec<T>::pack(cc);
             }
         }
     }
@@ -354,15 +670,183 @@ __global__ void __launch_bounds__(32 * kWarps) block_norm_backward_kernel(const 
     }
 }
 
+// The same with the rows' bulk copies kept in flight (see block_norm_rows_kernel).  A CTA's rows are of
+// one canvas; its groups take them in turn, and their columns' sums are added at the end, in the
+// order of the groups.
+template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas, bool kFull>
+__global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
+    block_norm_backward_rows_kernel(const __grid_constant__ BlockNormBackwardParams p, int slots) {
+    constexpr int kN = Vec<T>::kN, kP = kN / 2, kThreads = 32 * kW;
+    extern __shared__ __align__(128) uint8_t slots_mem[];
+    __shared__ Rings<kGroups> rings;
+    __shared__ __align__(16) float sh[kGroups][2][3 * kW];
+    const int group = threadIdx.x / kThreads, t = threadIdx.x % kThreads;
+    const int n_vec = kFull ? kNV * kThreads : p.d / kN, d = kFull ? kNV * kThreads * kN : p.d;
+    const int b = blockIdx.x / p.runs, part = blockIdx.x - b * p.runs;
+    const int rows = min(p.run_rows, p.C - part * p.run_rows), n = rows > group ? (rows - group + kGroups - 1) / kGroups : 0;
+    const int64_t r0 = static_cast<int64_t>(b) * p.C + part * p.run_rows + group;  // then every kGroups-th row
+    const bool pre = p.w_pre != nullptr, post = p.y != nullptr, up = p.dx_out != nullptr;
+    const float inv_d = 1.0f / static_cast<float>(d);
+    // a slot: the rows of dx_out, dh, x and y that the call has
+    const uint32_t row_bytes = static_cast<uint32_t>(d) * sizeof(T);
+    const uint32_t at_h = up ? row_bytes : 0, at_x = at_h + (pre ? row_bytes : 0), at_y = at_x + (pre ? row_bytes : 0);
+    const uint32_t slot_bytes = at_y + (post ? row_bytes : 0);
+    uint8_t* ring = slots_mem + group * slots * slot_bytes;
+    rings_init(rings);
+    int64_t next = r0;
+    const auto fetch = [&](int slot) {  // the next row, into a free slot
+        uint64_t* bar = &rings.full[group][slot];
+        uint8_t* dst = ring + slot * slot_bytes;
+        mbar_arrive_expect_tx(bar, slot_bytes);
+        if (up) bulk_load(dst, static_cast<const T*>(p.dx_out) + next * p.ld_dx_out, row_bytes, bar);
+        if (pre) {
+            bulk_load(dst + at_h, static_cast<const T*>(p.dh) + next * p.ld_dh, row_bytes, bar);
+            bulk_load(dst + at_x, static_cast<const T*>(p.x) + next * p.ld_x, row_bytes, bar);
+        }
+        if (post) bulk_load(dst + at_y, static_cast<const T*>(p.y) + next * p.ld_y, row_bytes, bar);
+        next += kGroups;
+    };
+    if (t == 0)
+        for (int i = 0; i < min(n, slots); ++i) fetch(i);
+    Pair wp[kNV][kP], wc[kNV][kP], acc_pre[kNV][kP], acc_post[kNV][kP];
+    const Pair scale = pair(p.res_scale, p.res_scale);
+#pragma unroll
+    for (int k = 0; k < kNV; ++k) {
+        const int c = t + k * kThreads;
+#pragma unroll
+        for (int i = 0; i < kP; ++i) wp[k][i] = wc[k][i] = acc_pre[k][i] = acc_post[k][i] = 0;
+        if (kFull || c < n_vec) {
+            if (pre) load_pairs(static_cast<const P*>(p.w_pre) + c * kN, wp[k]);
+            if (post) {
+                load_pairs(static_cast<const P*>(p.w_post) + c * kN, wc[k]);
+                Pair g[kP];
+                if (p.gate) load_pairs(static_cast<const P*>(p.gate) + static_cast<int64_t>(b) * d + c * kN, g);
+#pragma unroll
+                for (int i = 0; i < kP; ++i) wc[k][i] = mul2(wc[k][i], p.gate ? mul2(scale, g[i]) : scale);
+            }
+        }
+    }
+    const float* rstd_x = p.rstd_x + r0;
+    const float* rstd_y = p.rstd_y + r0;
+    float rx = 0.f, ry = 0.f;  // of the row at hand, read a row ahead
+    if (n > 0) {
+        if (pre) rx = *rstd_x;
+        if (post) ry = *rstd_y;
+    }
+    T* dxo = static_cast<T*>(p.dx) + r0 * d + t * kN;
+    T* dyo = static_cast<T*>(p.dy) + r0 * d + t * kN;
+    const uint8_t* src0 = ring + t * 16;
+    int slot = 0, phase = 0, parity = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i, parity ^= 1, dxo += kGroups * d, dyo += kGroups * d) {
+        const bool more = i + 1 < n;
+        rstd_x += kGroups;
+        rstd_y += kGroups;
+        const float rx_next = pre && more ? *rstd_x : 0.f, ry_next = post && more ? *rstd_y : 0.f;
+        const Pair rx2 = pair(rx, rx), ry2 = pair(ry, ry);
+        mbar_wait(&rings.full[group][slot], phase, &rings.wc);
+        const uint8_t* src = src0 + slot * slot_bytes;
+        // a vector's columns of the four rows (zero where the call has none)
+        const auto read = [&](int k, Pair(&g)[kP], Pair(&h)[kP], Pair(&x)[kP], Pair(&y)[kP]) {
+            const bool in = kFull || t + k * kThreads < n_vec;
+            const uint8_t* at = src + k * (16 * kThreads);
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            unpack_pairs<T>(in && up ? *reinterpret_cast<const uint4*>(at) : zero, g);
+            unpack_pairs<T>(in && pre ? *reinterpret_cast<const uint4*>(at + at_h) : zero, h);
+            unpack_pairs<T>(in && pre ? *reinterpret_cast<const uint4*>(at + at_x) : zero, x);
+            unpack_pairs<T>(in && post ? *reinterpret_cast<const uint4*>(at + at_y) : zero, y);
+        };
+        Pair sum0 = 0, sum1 = 0, sum2_ = 0;
+#pragma unroll
+        for (int k = 0; k < kNV; ++k) {
+            Pair g[kP], h[kP], x[kP], y[kP];
+            read(k, g, h, x, y);
+#pragma unroll
+            for (int j = 0; j < kP; ++j) {
+                const Pair tt = mul2(h[j], wp[k][j]), cy = mul2(wc[k][j], y[j]);
+                sum0 = fma2(tt, x[j], sum0);
+                sum1 = fma2(cy, fma2(rx2, tt, g[j]), sum1);
+                sum2_ = fma2(cy, x[j], sum2_);
+            }
+        }
+        float s[3] = {sum2(sum0), sum2(sum1), sum2(sum2_)};
+        group_sums<kW>(s, sh[group][parity], group);
+        if (kW == 1) group_barrier<kW>(group);
+        // past this barrier every thread is done with the row before: its slot is free
+        if (t == 0 && i > 0 && i - 1 + slots < n) fetch(slot == 0 ? slots - 1 : slot - 1);
+        // sums of t x, c y (dx' + rstd_x t), c y x: the means' rstd factors are put in here
+        const float m1 = rx * s[0] * inv_d, m2 = ry * fmaf(-rx * rx * m1, s[2], s[1]) * inv_d;
+        const float a = -rx * rx * m1, e = -ry * ry * m2;
+        const Pair a2 = pair(a, a), e2 = pair(e, e);
+#pragma unroll
+        for (int k = 0; k < kNV; ++k) {
+            if (kFull || t + k * kThreads < n_vec) {
+                // (read again: kept in registers, the row would spill)
+                Pair g[kP], h[kP], x[kP], y[kP], dx[kP], dy[kP];
+                read(k, g, h, x, y);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    dx[j] = fma2(a2, x[j], fma2(rx2, mul2(h[j], wp[k][j]), g[j]));
+                    acc_pre[k][j] = fma2(mul2(h[j], rx2), x[j], acc_pre[k][j]);
+                    const Pair u = mul2(dx[j], ry2);
+                    acc_post[k][j] = fma2(u, y[j], acc_post[k][j]);
+                    dy[j] = fma2(e2, y[j], mul2(wc[k][j], u));
+                }
+                *reinterpret_cast<uint4*>(dxo + k * (kN * kThreads)) = pack_pairs<T>(dx);
+                if (post) *reinterpret_cast<uint4*>(dyo + k * (kN * kThreads)) = pack_pairs<T>(dy);
+            }
+        }
+        rx = rx_next;
+        ry = ry_next;
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    rings_drain(rings, group, t == 0, n, slots);
+    grid_launch_dependents();
+    // the groups' sums, by way of the ring's memory: group 0 adds the others' to its own
+    for (int which = 0; which < 2; ++which) {
+        if (which == 0 ? !pre : !post) continue;
+        float* sums = reinterpret_cast<float*>(slots_mem);  // [kGroups - 1, d]
+        if (group > 0) {
+#pragma unroll
+            for (int k = 0; k < kNV; ++k) {
+                const int c = t + k * kThreads;
+                if (c < n_vec) {
+#pragma unroll
+                    for (int i = 0; i < kP; ++i)
+                        *reinterpret_cast<Pair*>(sums + (group - 1) * p.d + c * kN + 2 * i) = which == 0 ? acc_pre[k][i] : acc_post[k][i];
+                }
+            }
+        }
+        __syncthreads();
+        if (group == 0) {
+            float* out = (which == 0 ? p.part_pre : p.part_post) + static_cast<int64_t>(blockIdx.x) * p.d;
+#pragma unroll
+            for (int k = 0; k < kNV; ++k) {
+                const int c = t + k * kThreads;
+                if (c < n_vec) {
+#pragma unroll
+                    for (int i = 0; i < kP; ++i) {
+                        float lo, hi;
+                        unpair(which == 0 ? acc_pre[k][i] : acc_post[k][i], lo, hi);
+                        for (int q = 0; q < kGroups - 1; ++q) {
+                            const float2 o = *reinterpret_cast<const float2*>(sums + q * p.d + c * kN + 2 * i);
+                            lo += o.x;
+                            hi += o.y;
+                        }
+                        *reinterpret_cast<float2*>(out + c * kN + 2 * i) = make_float2(lo, hi);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
 __device__ __forceinline__ float4 add4(float4 a, float4 b) {
     return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-}
-__device__ __forceinline__ float4 shfl_add4(float4 v, int o) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
-    v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
-    return v;
 }
 __device__ __forceinline__ float4 param4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ float4 param4(const __nv_bfloat16* p) {
@@ -371,61 +855,66 @@ __device__ __forceinline__ float4 param4(const __nv_bfloat16* p) {
     return make_float4(f[0], f[1], f[2], f[3]);
 }
 
-// Adds the runs' partial sums.  One warp per four columns: `sub` lanes share a canvas (a power of
-// two), 32 / sub canvases at a time; every sum has a fixed order.
+// Adds the runs' partial sums, blockIdx.y 0: dw_pre, 1: dw_post and dgate.  A CTA takes 32 columns:
+// eight threads of four columns (a 128-byte line of a run's sums) by 32 lanes that share the runs.  Of
+// the lanes, `sub` (a power of two) share a canvas; every sum has a fixed order.
 template <typename P>
-__global__ void __launch_bounds__(128) block_norm_params_kernel(const __grid_constant__ BlockNormBackwardParams p, int sub) {
+__global__ void __launch_bounds__(256) block_norm_params_kernel(const __grid_constant__ BlockNormBackwardParams p, int sub) {
+    __shared__ float4 sh[32][8];
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+    const int c = blockIdx.x * 32 + tx * 4;
+    const bool in = c < p.d, post = p.w_pre == nullptr || blockIdx.y == 1;
+    const float* part = post ? p.part_post : p.part_pre;
+    if (!post) sub = 32;
+    const int canvases = post ? p.B : 1, runs = post ? p.runs : p.B * p.runs;
+    const int first = ty / sub, l = ty % sub;
+    float4 total = make_float4(0.f, 0.f, 0.f, 0.f);
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int c = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 4;
-    if (c >= p.d) return;
-    if (p.w_pre) {
+    for (int b0 = 0; b0 < canvases; b0 += 32 / sub) {  // one turn unless sub == 1
+        const int b = b0 + first;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int n = p.B * p.runs;
-#pragma unroll 4
-        for (int j = lane; j < n; j += 32) a = add4(a, __ldcg(reinterpret_cast<const float4*>(p.part_pre + static_cast<int64_t>(j) * p.d + c)));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) a = shfl_add4(a, o);
-        if (lane == 0) *reinterpret_cast<float4*>(p.dw_pre + c) = a;
-    }
-    if (p.y) {
-        const float4 w = param4(static_cast<const P*>(p.w_post) + c);
-        float4 total = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int first = lane / sub, l = lane % sub;
-        for (int b0 = 0; b0 < p.B; b0 += 32 / sub) {
-            const int b = b0 + first;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (b < p.B) {
-#pragma unroll 4
-                for (int j = l; j < p.runs; j += sub)
-                    a = add4(a, __ldcg(reinterpret_cast<const float4*>(p.part_post + (static_cast<int64_t>(b) * p.runs + j) * p.d + c)));
-            }
-            for (int o = sub >> 1; o > 0; o >>= 1) a = shfl_add4(a, o);
+        if (in && b < canvases) {
+            const float* src = part + static_cast<int64_t>(b) * runs * p.d + c;
+#pragma unroll 8
+            for (int j = l; j < runs; j += sub) a = add4(a, __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(j) * p.d)));
+        }
+        if (sub > 1) {
+            sh[ty][tx] = a;
+            __syncthreads();
+            if (l == 0)
+                for (int q = 1; q < sub; ++q) a = add4(a, sh[ty + q][tx]);
+            __syncthreads();
+        }
+        if (l != 0 || !in || b >= canvases) continue;
+        if (post) {
             a = make_float4(p.res_scale * a.x, p.res_scale * a.y, p.res_scale * a.z, p.res_scale * a.w);
-            if (p.gate && b < p.B) {
+            if (p.gate) {
                 const int64_t at = static_cast<int64_t>(b) * p.d + c;
-                const float4 g = param4(static_cast<const P*>(p.gate) + at);
-                if (l == 0) *reinterpret_cast<float4*>(p.dgate + at) = make_float4(w.x * a.x, w.y * a.y, w.z * a.z, w.w * a.w);
+                const float4 g = param4(static_cast<const P*>(p.gate) + at), w = param4(static_cast<const P*>(p.w_post) + c);
+                *reinterpret_cast<float4*>(p.dgate + at) = make_float4(w.x * a.x, w.y * a.y, w.z * a.z, w.w * a.w);
                 a = make_float4(g.x * a.x, g.y * a.y, g.z * a.z, g.w * a.w);
             }
-            total = add4(total, a);
         }
-        for (int o = 16; o >= sub; o >>= 1) total = shfl_add4(total, o);
-        if (lane == 0) *reinterpret_cast<float4*>(p.dw_post + c) = total;
+        total = add4(total, a);
+    }
+    sh[ty][tx] = total;
+    __syncthreads();
+    if (ty == 0 && in) {
+        for (int q = sub; q < 32; q += sub) total = add4(total, sh[q][tx]);
+        *reinterpret_cast<float4*>((post ? p.dw_post : p.dw_pre) + c) = total;
     }
 }
 
-template <typename T, typename P, int kWarps, int kNV>
-cudaError_t launch_backward(const BlockNormBackwardParams& p, cudaStream_t st) {
-    block_norm_backward_kernel<T, P, kWarps, kNV><<<static_cast<unsigned>(p.B) * p.runs, 32 * kWarps, 0, st>>>(p);
+template <typename P>
+cudaError_t launch_params(const BlockNormBackwardParams& p, cudaStream_t st) {
     note_launches(1);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    int sub = 32;  // lanes per canvas: as many as keep a canvas for every group of lanes
+    int sub = 32;  // lanes per canvas: as many as leave a group of lanes for every canvas
     while (sub > 1 && 32 / sub < p.B) sub >>= 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.d / 4 + 3) / 4));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(static_cast<unsigned>((p.d + 31) / 32), p.w_pre && p.y ? 2u : 1u);
+    cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -438,20 +927,61 @@ cudaError_t launch_backward(const BlockNormBackwardParams& p, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <typename T, typename P, int kWarps, int kNV>
+cudaError_t launch_backward(const BlockNormBackwardParams& p, cudaStream_t st) {
+    block_norm_backward_kernel<T, P, kWarps, kNV><<<static_cast<unsigned>(p.B) * p.runs, 32 * kWarps, 0, st>>>(p);
+    return launch_params<P>(p, st);
+}
+
+template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas, bool kFull>
+cudaError_t launch_backward_rows_as(const BlockNormBackwardParams& p, cudaStream_t st) {
+    constexpr int kRingBytes = 200 * 1024 / kCtas;
+    const int slot = p.d * static_cast<int>(sizeof(T)) * ((p.dx_out ? 1 : 0) + (p.w_pre ? 2 : 0) + (p.y ? 1 : 0));
+    const int slots = std::min(kMaxSlots, kRingBytes / (slot * kGroups));
+    const int bytes = std::max(kGroups * slots * slot, (kGroups - 1) * p.d * 4);
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [] {
+        attr_err = cudaFuncSetAttribute(block_norm_backward_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    block_norm_backward_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull><<<static_cast<unsigned>(p.B) * p.runs, 32 * kW * kGroups, bytes, st>>>(p, slots);
+    return launch_params<P>(p, st);
+}
+
+template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas>
+cudaError_t launch_backward_rows(const BlockNormBackwardParams& p, cudaStream_t st) {
+    if (p.d == kNV * kW * 32 * Vec<T>::kN) return launch_backward_rows_as<T, P, kW, kGroups, kNV, kCtas, true>(p, st);
+    return launch_backward_rows_as<T, P, kW, kGroups, kNV, kCtas, false>(p, st);
+}
+
 template <typename T, typename P>
 cudaError_t backward_by_width(const BlockNormBackwardParams& p, cudaStream_t st) {
     const int n_vec = p.d / Vec<T>::kN;
-    if (n_vec <= 32) return launch_backward<T, P, 1, 1>(p, st);
-    if (n_vec <= 64) return launch_backward<T, P, 2, 1>(p, st);
-    if (n_vec <= 128) return launch_backward<T, P, 4, 1>(p, st);
-    if (n_vec <= 256) return launch_backward<T, P, 8, 1>(p, st);
-    if (n_vec <= 512) return launch_backward<T, P, 16, 1>(p, st);
-    if (n_vec <= 1024) return launch_backward<T, P, 16, 2>(p, st);
-    if (n_vec <= 2048) return launch_backward<T, P, 32, 2>(p, st);
-    return launch_backward<T, P, 32, 4>(p, st);
+    if (n_vec <= 32) return launch_backward_rows<T, P, 1, 8, 1, kNormCtas>(p, st);
+    if (n_vec <= 64) return launch_backward_rows<T, P, 1, 8, 2, kNormCtas>(p, st);
+    if (n_vec <= 128) return launch_backward_rows<T, P, 2, 4, 2, kNormCtas>(p, st);
+    if (n_vec <= 256) return launch_backward_rows<T, P, 4, 2, 2, kNormCtas>(p, st);
+    if (n_vec <= 512) return launch_backward_rows<T, P, 8, 1, 2, kNormCtas>(p, st);
+    if (n_vec <= 1024) return launch_backward_rows<T, P, 16, 1, 2, 1>(p, st);
+    if constexpr (sizeof(T) == 4)  // (bf16 rows have 2048 vectors at most)
+        if (n_vec > 2048) return launch_backward<T, P, 16, 8>(p, st);
+    return launch_backward<T, P, 16, 4>(p, st);
 }
 
 }  // namespace
+
+cudaError_t read_and_clear_norm_error(int* out) {
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int));
+    if (e != cudaSuccess) return e;
+    if (v) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
+    }
+    *out = v;
+    return e;
+}
 
 cudaError_t launch_block_norm(const BlockNormParams& p, int act_bf16, int param_bf16, cudaStream_t st) {
     if (act_bf16)
@@ -459,10 +989,12 @@ cudaError_t launch_block_norm(const BlockNormParams& p, int act_bf16, int param_
     return param_bf16 ? forward_by_width<float, __nv_bfloat16>(p, st) : forward_by_width<float, float>(p, st);
 }
 
-// Runs of rows per canvas: about four CTAs of work per SM, never more runs than rows.
-int32_t block_norm_runs(int32_t B, int32_t C) {
-    const int want = (4 * num_sms() + B - 1) / B;
-    return std::max(1, std::min<int32_t>(want, C));
+// Runs of rows per canvas: as many CTAs as the SMs hold at once, but two rows to a run, so that there
+// are not more partial sums than need be (256 rows of 2048 in runs of one, two, four: 11.9, 9.4, 9.8 us).
+int32_t block_norm_runs(int32_t B, int32_t C, int32_t d, int act_bf16) {
+    const int n_vec = d / (act_bf16 ? 8 : 4);
+    const int per_sm = n_vec <= 512 ? kNormCtas : 1;
+    return std::max(1, std::min<int32_t>(per_sm * num_sms() / B, (C + 1) / 2));
 }
 
 cudaError_t launch_block_norm_backward(const BlockNormBackwardParams& p, int act_bf16, int param_bf16, cudaStream_t st) {

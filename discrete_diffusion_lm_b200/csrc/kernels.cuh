@@ -166,7 +166,7 @@ struct BlockNormBackwardParams {
     float *dw_post, *dgate, *dw_pre;
     float *part_pre, *part_post;  // [B * runs, d] partial sums
 };
-int32_t block_norm_runs(int32_t B, int32_t C);
+int32_t block_norm_runs(int32_t B, int32_t C, int32_t d, int act_bf16);
 cudaError_t launch_block_norm_backward(const BlockNormBackwardParams& p, int act_bf16, int param_bf16, cudaStream_t s);
 
 // Microscaled 4-bit floating point (mx4.cu): scale tiles, quantisation, reading back, products.
@@ -190,6 +190,7 @@ struct Mx4MatmulParams {
 };
 cudaError_t launch_mx4_matmul(const Mx4MatmulParams& p, cudaStream_t s);
 cudaError_t read_and_clear_mx4_error(int* out);
+cudaError_t read_and_clear_norm_error(int* out);
 
 // The sampler step behind the two C entry points (dg_sampler_step, dg_sampler_step_noalloc): all
 // arguments are checked first; with clear_ws the workspace is then zeroed on the stream before the

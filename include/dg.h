@@ -366,7 +366,8 @@ int dg_block_norm(const void* x, int64_t ld_x, const void* y, int64_t ld_y, int 
 /* Workspace: dg_block_norm_backward_workspace_size bytes, 16-byte aligned, */
 /* any contents.  Two launches.                                              */
 /* ------------------------------------------------------------------------ */
-size_t dg_block_norm_backward_workspace_size(int32_t B, int32_t C, int32_t d, int have_gate);
+size_t dg_block_norm_backward_workspace_size(int32_t B, int32_t C, int32_t d, int act_dtype,
+                                             int have_gate);
 
 int dg_block_norm_backward(const void* dx_out, int64_t ld_dx_out, const void* dh, int64_t ld_dh,
                            const void* x, int64_t ld_x, const void* y, int64_t ld_y, int act_dtype,

@@ -147,8 +147,8 @@ def test_sizes(L):
     assert L.dg_ffw_mx4_workspace_size(0, 64, 64) == 0
     assert L.dg_ffw_mx4_workspace_size(256, 2048, 8192) >= 256 * (2048 + 8192) * 17 // 32
     w = L.dg_block_norm_backward_workspace_size
-    assert w(0, 4, 64, 1) == 0 and w(1, 1, 64, 1) == 2 * 64 * 4
-    assert w(8, 1536, 2048, 1) >= 2 * 8 * 2048 * 4
+    assert w(0, 4, 64, 1, 1) == 0 and w(1, 1, 64, 1, 1) == 2 * 64 * 4 and w(1, 1, 64, 5, 1) == 0
+    assert w(8, 1536, 2048, 1, 1) >= 2 * 8 * 2048 * 4
 
 
 def test_binding_rejects_before_any_call(L):
