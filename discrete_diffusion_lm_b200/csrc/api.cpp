@@ -211,8 +211,9 @@ NormRuns norm_runs(int32_t B, int32_t C, int32_t d, int act_dtype, bool have_gat
 }
 
 int check_mx4_matrix(int32_t rows, int32_t K) {
-    if (rows < 1) return fail(DG_ERR_INVALID_ARG, "the row count %d must be >= 1", rows);
+    if (rows < 1 || rows > 0x7fffff00) return fail(DG_ERR_INVALID_ARG, "the row count %d must be in [1, 2^31 - 256]", rows);
     if (K < 32 || K % 32 != 0) return fail(DG_ERR_INVALID_ARG, "K = %d must be a positive multiple of 32", K);
+    if (K > (1 << 24)) return fail(DG_ERR_INVALID_ARG, "K = %d exceeds 2^24", K);
     return DG_OK;
 }
 
@@ -970,7 +971,7 @@ int dg_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, c
         return fail(DG_ERR_INVALID_ARG, "a, a_scales, w, w_scales and out are required");
     if (!valid_dtype(out_dtype)) return fail(DG_ERR_INVALID_ARG, "out dtype %d is not DG_F32 or DG_BF16", out_dtype);
     if ((rc = check_mx4_matrix(M, K)) != DG_OK) return rc;
-    if (N < 8 || N % 8 != 0) return fail(DG_ERR_INVALID_ARG, "N = %d must be a positive multiple of 8", N);
+    if (N < 8 || N % 8 != 0 || N > 0x7fffff00) return fail(DG_ERR_INVALID_ARG, "N = %d must be a positive multiple of 8 below 2^31 - 256", N);
     if (!aligned16(a) || !aligned16(a_scales) || !aligned16(w) || !aligned16(w_scales) || !aligned16(out))
         return fail(DG_ERR_ALIGNMENT, "all operands must be 16-byte aligned");
     if ((rc = check_device()) != DG_OK) return rc;
