@@ -1016,12 +1016,18 @@ int dg_ffw_mx4(const void* z_in, int32_t rows, int32_t d, int32_t d_ff, const ui
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     uint8_t *zq = ws, *zs = zq + n.z_codes, *hq = zs + n.z_scales, *hs = hq + n.h_codes;
-    cudaError_t e = launch_mx4_quantize(z_in, d, 1, rows, d, zq, zs, s);
-    if (e != cudaSuccess) return cuda_fail(e, "FFW input quantisation launch");
     Mx4MatmulParams p;
     std::memset(&p, 0, sizeof(p));
-    p.a = zq;
-    p.a_scales = zs;
+    cudaError_t e = cudaSuccess;
+    if (rows <= kMx4FewRows) {
+        p.a_bf16 = z_in;
+    } else {
+        e = launch_mx4_quantize(z_in, d, 1, rows, d, zq, zs, s);
+        if (e != cudaSuccess) return cuda_fail(e, "FFW input quantisation launch");
+        p.a = zq;
+        p.a_scales = zs;
+        p.dependent = 1;
+    }
     p.w = w1;
     p.w_scales = w1_scales;
     p.M = rows;
@@ -1030,9 +1036,10 @@ int dg_ffw_mx4(const void* z_in, int32_t rows, int32_t d, int32_t d_ff, const ui
     p.out_kind = kMx4OutGelu;
     p.out = hq;
     p.out_scales = hs;
-    p.dependent = 1;
     e = launch_mx4_matmul(p, s);
     if (e != cudaSuccess) return cuda_fail(e, "FFW layer 1 launch");
+    p.a_bf16 = nullptr;
+    p.dependent = 1;
     p.a = hq;
     p.a_scales = hs;
     p.w = w2;

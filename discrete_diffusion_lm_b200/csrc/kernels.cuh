@@ -180,9 +180,13 @@ enum Mx4OutKind : int {
     kMx4OutF32 = 1,
     kMx4OutGelu = 2,  // gelu of the product, quantised again
 };
+// Up to so many rows the product quantises a bf16 A itself: beyond, a launch of its own costs less than
+// every column tile's doing it again.
+constexpr int32_t kMx4FewRows = 32;
 struct Mx4MatmulParams {
     const uint8_t *a, *a_scales, *w, *w_scales;
     int32_t M, N, K;
+    const void* a_bf16;   // kMx4OutGelu and at most kMx4FewRows rows: A as bf16 [M, K] instead of a, a_scales
     int32_t out_kind;
     void* out;            // [M, N] bf16 or fp32, or codes [M, N / 2]
     uint8_t* out_scales;  // kMx4OutGelu

@@ -187,6 +187,8 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* __re
 // tcgen05.mma.kind::mxf4 of K = 64, two scale bytes per row and instruction.  (tcgen05.cp and the
 // products that follow it in one thread run one after the other: with both in one thread a stage took
 // 1100 to 1300 cycles instead of about 560.)
+// With few rows A may be bf16 (kFew): the epilogue's warps, idle until the products are done, quantise
+// each stage of it into shared memory, a block of 32 values per thread, in the place of its copies.
 // With few tiles K is split over the CTAs of a cluster: each sends every other its share of the rows
 // of its fp32 tile (bulk copies into that CTA's inbox), and adds the shares it is sent in a fixed order.
 constexpr int kMTile = 128, kNTile = 128, kKStage = 256;
@@ -209,6 +211,7 @@ enum Mx4Out : int { kOutBf16 = 0, kOutF32 = 1, kOutGeluMx4 = 2 };
 struct alignas(64) Mx4Kernel {
     CUtensorMap tm_a, tm_w;  // bytes [rows, K / 2], box 128 rows x 128 bytes
     const uint8_t *sa, *sw;
+    const __nv_bfloat16* a_bf16;  // kFew: A [M, K]
     void* out;            // bf16 or fp32 [M, N], or codes [M, N / 2]
     uint8_t* out_scales;  // kOutGeluMx4
     int32_t M, N, K;
@@ -282,7 +285,31 @@ __device__ __forceinline__ float max_abs_nan(float a, float b) {
     return r;
 }
 
-template <int kOut>
+// Sixteen bytes of codes and the scale byte of a block of 32 bf16 values.
+__device__ __forceinline__ uint4 quantize_block(const __nv_bfloat16* x, uint32_t& c) {
+    uint32_t w[16], q[4], top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(x) + i);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, max(w[i] << 16 & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+    c = scale_byte(top);
+    const float inv = inverse_scale(c == 255u ? kUnitScale : c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float f[8] = {bf16_lo(w[4 * i]),     bf16_hi(w[4 * i]),     bf16_lo(w[4 * i + 1]), bf16_hi(w[4 * i + 1]),
+                            bf16_lo(w[4 * i + 2]), bf16_hi(w[4 * i + 2]), bf16_lo(w[4 * i + 3]), bf16_hi(w[4 * i + 3])};
+        q[i] = c == 255u ? 0u : pack_e2m1(f, inv);
+    }
+    return make_uint4(q[0], q[1], q[2], q[3]);
+}
+
+template <int kOut, bool kFew>
 __global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid_constant__ Mx4Kernel p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -314,9 +341,13 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid
         bulk_load(st + 2 * kOperandBytes + (is_a ? 0 : kScaleBytes),
                   (is_a ? p.sa : p.sw) + static_cast<int64_t>(rt) * p.k_tiles * 512 + static_cast<int64_t>(kb) * 1024, scale_bytes, bar);
     };
+    if (threadIdx.x == 96) {
+        prefetch_map(&p.tm_w);
+        if (!kFew) prefetch_map(&p.tm_a);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMx4Stages; ++s) {
-            mbar_init(&full[s], 2);
+            mbar_init(&full[s], kFew ? 9 : 2);  // W's copies, and A's or the eight warps that write it
             mbar_init(&scaled[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -341,7 +372,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid
     }
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
-    if ((warp == 0 || warp == 2) && lane == 0) {
+    if ((warp == 0 || (warp == 2 && !kFew)) && lane == 0) {
         // ---------------------------------------------------------------- producers: W, A
         const bool is_a = warp == 2;
         int32_t kb = kb0;
@@ -413,6 +444,31 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid
         }
     }
     __syncwarp();
+    if (kFew && warp >= 4) {
+        // ---------------------------------------------------------------- A, quantised
+        int s = 0, phase = 0;
+        for (int32_t kb = kb0; kb < kb1; ++kb) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], phase ^ 1, wc))) break;
+            uint8_t* st = smem + s * kStageBytes;
+            for (int i = threadIdx.x - 128; i < m_valid * 8; i += 256) {
+                const int row = i >> 3, j = i & 7;  // the stage's block j of a row: its 16-byte chunk j
+                const int32_t k = kb * kKStage + j * 32;
+                uint4 q = make_uint4(0, 0, 0, 0);
+                uint32_t c = kUnitScale;
+                if (k < p.K) q = quantize_block(p.a_bf16 + (static_cast<int64_t>(mt) * kMTile + row) * p.K + k, c);
+                *reinterpret_cast<uint4*>(st + row * 128 + ((j ^ (row & 7)) << 4)) = q;
+                st[2 * kOperandBytes + (j >> 2) * 512 + (row & 31) * 16 + (row >> 5) * 4 + (j & 3)] = static_cast<uint8_t>(c);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1;
+            }
+        }
+        __syncwarp();
+    }
 
     // ---------------------------------------------------------------- epilogue: fp32 tile, then rows
     float* tile_f = reinterpret_cast<float*>(smem);
@@ -515,12 +571,12 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
-template <int kOut>
+template <int kOut, bool kFew = false>
 cudaError_t launch_product(const Mx4Kernel& kp, int grid, int splits, bool dependent, cudaStream_t st) {
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(mx4_matmul_kernel<kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMx4Smem));
+        attr_err = cudaFuncSetAttribute(mx4_matmul_kernel<kOut, kFew>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMx4Smem));
     });
     if (attr_err != cudaSuccess) return attr_err;
     cudaLaunchConfig_t cfg = {};
@@ -536,7 +592,7 @@ cudaError_t launch_product(const Mx4Kernel& kp, int grid, int splits, bool depen
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = dependent ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, mx4_matmul_kernel<kOut>, kp);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, mx4_matmul_kernel<kOut, kFew>, kp);
     if (e != cudaSuccess) return e;
     note_launches(1);
     return cudaGetLastError();
@@ -789,11 +845,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (kOut == kOutGeluMx4) {
                 const bool valid = row0 + row < p.M;
                 const int64_t r = row0 + row;
-                uint32_t word = 0;
-#pragma unroll 1
+                uint32_t word = 0, all[kCols];
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) tmem_ld_32x32b_x32_nowait(acc + c, all + c);
+                tmem_ld_wait();
+                tcgen05_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(leader_empty + b * 8);
+#pragma unroll
                 for (int c = 0; c < kCols; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(acc + c, v);
+                    const uint32_t* v = all + c;
                     float f[32], most[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int q = 0; q < 32; ++q) {
@@ -827,9 +888,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         word = 0;
                     }
                 }
-                tcgen05_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(leader_empty + b * 8);
             } else {
                 constexpr int kSlabCols = kOut == kOutBf16 ? 64 : 32;
                 constexpr int kBatches = kCols / (kSlabCols * G::kSlabs) > 0 ? kCols / (kSlabCols * G::kSlabs) : 1;
@@ -1001,12 +1059,14 @@ cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
     }
     Mx4Kernel kp;
     std::memset(&kp, 0, sizeof(kp));
-    cudaError_t e = encode_2d(&kp.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.a, q.K / 2, q.M, q.K / 2, 128, kMTile, CU_TENSOR_MAP_SWIZZLE_128B);
+    cudaError_t e = cudaSuccess;
+    if (!q.a_bf16) e = encode_2d(&kp.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.a, q.K / 2, q.M, q.K / 2, 128, kMTile, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e == cudaSuccess)
         e = encode_2d(&kp.tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.w, q.K / 2, q.N, q.K / 2, 128, kNTile, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
     kp.sa = q.a_scales;
     kp.sw = q.w_scales;
+    kp.a_bf16 = static_cast<const __nv_bfloat16*>(q.a_bf16);
     kp.out = q.out;
     kp.out_scales = q.out_scales;
     kp.M = q.M;
@@ -1020,6 +1080,7 @@ cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (q.out_kind == kMx4OutF32) return launch_product<kOutF32>(kp, static_cast<int>(grid), splits, q.dependent != 0, st);
     if (q.out_kind == kMx4OutBf16) return launch_product<kOutBf16>(kp, static_cast<int>(grid), splits, q.dependent != 0, st);
+    if (q.a_bf16) return launch_product<kOutGeluMx4, true>(kp, static_cast<int>(grid), splits, q.dependent != 0, st);
     return launch_product<kOutGeluMx4>(kp, static_cast<int>(grid), splits, q.dependent != 0, st);
 }
 

@@ -349,7 +349,8 @@ def check_block(z, w1, w1v, w2, w2v, got):
     return (slack > 0).double().mean().item()
 
 
-@pytest.mark.parametrize("R,d,dff", [(1, 64, 64), (16, 64, 256), (5, 192, 320), (1, 1024, 4096), (130, 512, 2048), (256, 2048, 8192), (300, 128, 576), (2500, 320, 2112), (1100, 1024, 4096)])
+@pytest.mark.parametrize("R,d,dff", [(1, 64, 64), (16, 64, 256), (5, 192, 320), (1, 1024, 4096), (130, 512, 2048), (256, 2048, 8192), (300, 128, 576), (2500, 320, 2112), (1100, 1024, 4096),
+                                     (32, 2048, 8192), (33, 2048, 8192), (31, 192, 64), (17, 4160, 128)])
 def test_block(R, d, dff):
     g = gen(R + d)
     z = randn(g, R, d, dtype=BF16)
@@ -476,6 +477,7 @@ def test_launch_counts():
     assert count(lambda: dg.dg_block_norm(x, w)) == 1
     assert count(lambda: dg.dg_mx4_quantize(x)) == 1
     assert count(lambda: dg.dg_mx4_matmul(w1, w1)) == 1
-    assert count(lambda: dg.dg_ffw_mx4(x, w1, w1)) == 3
+    assert count(lambda: dg.dg_ffw_mx4(x, w1, w1)) == 2
+    assert count(lambda: dg.dg_ffw_mx4(x.repeat(5, 1), w1, w1)) == 3
     r = dg.dg_block_norm(x, w)["rstd_x"]
     assert count(lambda: dg.dg_block_norm_backward(None, x, x, w, rstd_x=r)) == 2
