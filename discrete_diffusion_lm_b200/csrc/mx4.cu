@@ -615,8 +615,7 @@ struct PairTile {
     static constexpr uint32_t kSwBytes = (kN / 128) * kScaleBytes;
     static constexpr uint32_t kStage = kABytes + kWBytes + kScaleBytes + kSwBytes;
     static constexpr uint32_t kSlabBytes = 16384;            // 128 rows x 128 bytes
-    static constexpr int kSlabs = kN / 128;                  // per epilogue group: its columns in bf16
-    static constexpr uint32_t kStaging = 2 * kSlabs * kSlabBytes;
+    static constexpr uint32_t kStaging = 2 * kSlabBytes;  // one per epilogue group: a fifth stage is worth more
     static constexpr uint32_t kBudget = 226u * 1024u;
     static constexpr int kFit = static_cast<int>((kBudget - kStaging) / kStage);
     static constexpr int kStages = kFit > 8 ? 8 : kFit;
@@ -827,7 +826,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int row = quarter * 32 + lane;
         const bool issuer = threadIdx.x == 64 + 128 * group;
         const uint32_t leader_empty = map_to_rank(smem_u32(&acc_empty[0]), 0);
-        const uint32_t area = smem_u32(staging) + group * G::kSlabs * G::kSlabBytes;
+        const uint32_t area = smem_u32(staging) + group * G::kSlabBytes;
         const uint32_t row_base = area + row * 128;
         const uint32_t sw = row & 7;
         constexpr int kCols = kN / 2;  // of the group
@@ -836,8 +835,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int32_t nt = t / p.m_tiles, mt = t - nt * p.m_tiles;
             const int b = n % G::kBuffers;
             const bool got = mbar_wait(&acc_full[b], (n / G::kBuffers) & 1, wc);
-            if (issuer) bulk_wait_read_all();  // the slabs of the tile before have been read
-            if (group_sync_or(group, !got)) break;
+            if (group_sync_or(group, !got)) break;  // (and the issuer has seen the last slab read out)
             tcgen05_after_sync();
             const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * kN + group * kCols;
             const int32_t row0 = (2 * mt + static_cast<int32_t>(rank)) * 128;
@@ -889,11 +887,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     }
                 }
             } else {
+                // The whole share of the accumulator goes to registers first: the next tile's products wait
+                // only for that.  Then slab by slab through shared memory, in boxes of 32 rows with one in
+                // flight: a burst of stores would hold up the copies behind it (42 us instead of 35).
                 constexpr int kSlabCols = kOut == kOutBf16 ? 64 : 32;
-                constexpr int kBatches = kCols / (kSlabCols * G::kSlabs) > 0 ? kCols / (kSlabCols * G::kSlabs) : 1;
-                constexpr int kSlabsUsed = kCols / (kSlabCols * kBatches);
-                // the whole share of the accumulator goes to registers first: the next tile's products wait
-                // only for that
                 uint32_t v[kCols];
 #pragma unroll
                 for (int c = 0; c < kCols; c += 32) tmem_ld_32x32b_x32_nowait(acc + c, v + c);
@@ -902,19 +899,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(leader_empty + b * 8);
 #pragma unroll
-                for (int batch = 0; batch < kBatches; ++batch) {
-                    if (batch > 0) {  // the previous batch has been read out before its slabs are overwritten
-                        if (issuer) bulk_wait_read_all();
-                        group_sync_or(group, false);
-                    }
+                for (int s0 = 0; s0 < kCols; s0 += kSlabCols) {
+                    if (s0 > 0) group_sync_or(group, false);  // the issuer has seen the slab before read out
 #pragma unroll
-                    for (int c = 0; c < kSlabsUsed * kSlabCols; c += 32) {
-                        const uint32_t* w = v + batch * kSlabsUsed * kSlabCols + c;
-                        const uint32_t slab = row_base + (c / kSlabCols) * G::kSlabBytes;
+                    for (int c = 0; c < kSlabCols; c += 32) {
+                        const uint32_t* w = v + s0 + c;
                         if (kOut == kOutBf16) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                st_shared_v4(slab + ((((c & 32) / 8 + k) ^ sw) << 4),
+                                st_shared_v4(row_base + (((c / 8 + k) ^ sw) << 4),
                                              make_uint4(pack_bf16x2(__uint_as_float(w[8 * k]), __uint_as_float(w[8 * k + 1])),
                                                         pack_bf16x2(__uint_as_float(w[8 * k + 2]), __uint_as_float(w[8 * k + 3])),
                                                         pack_bf16x2(__uint_as_float(w[8 * k + 4]), __uint_as_float(w[8 * k + 5])),
@@ -922,22 +915,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         } else {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                st_shared_v4(slab + ((k ^ sw) << 4), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+                                st_shared_v4(row_base + ((k ^ sw) << 4), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
                         }
                     }
                     fence_proxy_async_smem();
                     group_sync_or(group, false);
-                    if (issuer && row0 < p.M) {
-#pragma unroll
-                        for (int j = 0; j < kSlabsUsed; ++j) {
-                            const int32_t col = col0 + (batch * kSlabsUsed + j) * kSlabCols;
-                            if (col >= p.N) break;
+                    if (issuer && col0 + s0 < p.N) {
 #pragma unroll 1
-                            for (int q = 0; q < 4 && row0 + 32 * q < p.M; ++q) {
-                                tma_store_2d(&p.tm_out, col, row0 + 32 * q, area + j * G::kSlabBytes + q * 4096);
-                                bulk_commit();
-                                bulk_wait_read_all();
-                            }
+                        for (int q = 0; q < 4 && row0 + 32 * q < p.M; ++q) {
+                            tma_store_2d(&p.tm_out, col0 + s0, row0 + 32 * q, area + q * 4096);
+                            bulk_commit();
+                            bulk_wait_read_all();
                         }
                     }
                 }
