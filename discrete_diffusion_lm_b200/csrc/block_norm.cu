@@ -397,19 +397,19 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
     const float inv_d = 1.0f / static_cast<float>(d);
     uint8_t* ring = slots_mem + group * slots * slot_bytes;
     rings_init(rings);
-    const T* next_x = static_cast<const T*>(p.x) + static_cast<int64_t>(r0) * p.ld_x;
-    const T* next_y = static_cast<const T*>(p.y) + static_cast<int64_t>(r0) * p.ld_y;
+    const int ahead = min(n, slots);  // rows fetched before the walk; slot s is always filled by thread s
+    const T* next_x = static_cast<const T*>(p.x) + (static_cast<int64_t>(r0) + (t < ahead ? t : 0)) * p.ld_x;
+    const T* next_y = static_cast<const T*>(p.y) + (static_cast<int64_t>(r0) + (t < ahead ? t : 0)) * p.ld_y;
     const auto fetch = [&](int slot) {  // the next row, into a free slot
         uint64_t* bar = &rings.full[group][slot];
         uint8_t* dst = ring + slot * slot_bytes;
         mbar_arrive_expect_tx(bar, slot_bytes);
         bulk_load(dst, next_x, row_bytes, bar);
         if (post) bulk_load(dst + row_bytes, next_y, row_bytes, bar);
-        next_x += p.ld_x;
-        next_y += p.ld_y;
+        next_x += slots * p.ld_x;
+        next_y += slots * p.ld_y;
     };
-    if (t == 0)
-        for (int i = 0; i < min(n, slots); ++i) fetch(i);
+    if (t < ahead) fetch(t);
     Pair wc[kNV][kP], wpre[kNV][kP];  // res_scale gate w_post, w_pre
     int canvas = r0 / p.C, left = 0;  // rows before wc is of the next canvas
     const auto load_post = [&]() {
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
         if (pre) rstd = group_rstd<T, kW>(fx, inv_d, p.eps, sh[group][1], sh64[group], group);
         // between this barrier and the last row's, the slot and the exchange's floats have been read
         if (kW == 1 || !post || !pre) group_barrier<kW>(group);
-        if (t == 0 && i + slots < n) fetch(slot);
+        if (t == slot && i + slots < n) fetch(slot);
         if (pre) {
             if (t == 0 && p.rstd_x) p.rstd_x[r0 + i] = rstd;
             const Pair rstd2 = pair(rstd, rstd);
@@ -693,7 +693,8 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
     const uint32_t slot_bytes = at_y + (post ? row_bytes : 0);
     uint8_t* ring = slots_mem + group * slots * slot_bytes;
     rings_init(rings);
-    int64_t next = r0;
+    const int ahead = min(n, slots);  // rows fetched before the walk; slot s is always filled by thread s
+    int64_t next = r0 + (t < ahead ? t : 0) * kGroups;
     const auto fetch = [&](int slot) {  // the next row, into a free slot
         uint64_t* bar = &rings.full[group][slot];
         uint8_t* dst = ring + slot * slot_bytes;
@@ -704,10 +705,9 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
             bulk_load(dst + at_x, static_cast<const T*>(p.x) + next * p.ld_x, row_bytes, bar);
         }
         if (post) bulk_load(dst + at_y, static_cast<const T*>(p.y) + next * p.ld_y, row_bytes, bar);
-        next += kGroups;
+        next += slots * kGroups;
     };
-    if (t == 0)
-        for (int i = 0; i < min(n, slots); ++i) fetch(i);
+    if (t < ahead) fetch(t);
     Pair wp[kNV][kP], wc[kNV][kP], acc_pre[kNV][kP], acc_post[kNV][kP];
     const Pair scale = pair(p.res_scale, p.res_scale);
 #pragma unroll
@@ -773,7 +773,8 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
         group_sums<kW>(s, sh[group][parity], group);
         if (kW == 1) group_barrier<kW>(group);
         // past this barrier every thread is done with the row before: its slot is free
-        if (t == 0 && i > 0 && i - 1 + slots < n) fetch(slot == 0 ? slots - 1 : slot - 1);
+        const int before = slot == 0 ? slots - 1 : slot - 1;
+        if (t == before && i > 0 && i - 1 + slots < n) fetch(before);
         // sums of t x, c y (dx' + rstd_x t), c y x: the means' rstd factors are put in here
         const float m1 = rx * s[0] * inv_d, m2 = ry * fmaf(-rx * rx * m1, s[2], s[1]) * inv_d;
         const float a = -rx * rx * m1, e = -ry * ry * m2;
