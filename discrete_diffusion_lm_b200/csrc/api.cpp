@@ -963,8 +963,11 @@ int dg_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows,
     return DG_OK;
 }
 
-int dg_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales, int32_t M, int32_t N,
-                  int32_t K, void* out, int out_dtype, dg_stream_t stream) {
+}  // extern "C"
+
+namespace {
+int mx4_matmul_impl(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales, int32_t M, int32_t N,
+                    int32_t K, void* out, int out_dtype, dg_stream_t stream, int32_t fault_block, long long wait_limit) {
     g_last_error.clear();
     int rc;
     if (!a || !a_scales || !w || !w_scales || !out)
@@ -986,9 +989,28 @@ int dg_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, c
     p.K = K;
     p.out_kind = out_dtype == DG_BF16 ? kMx4OutBf16 : kMx4OutF32;
     p.out = out;
+    p.fault_block = fault_block;
+    p.wait_limit = wait_limit;
     const cudaError_t e = launch_mx4_matmul(p, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "4-bit product launch");
     return DG_OK;
+}
+}  // namespace
+
+extern "C" {
+
+int dg_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales, int32_t M, int32_t N,
+                  int32_t K, void* out, int out_dtype, dg_stream_t stream) {
+    return mx4_matmul_impl(a, a_scales, w, w_scales, M, N, K, out, out_dtype, stream, -1, 0);
+}
+
+int dg_test_mx4_stall(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales, int32_t M, int32_t N,
+                      int32_t K, void* out, int out_dtype, dg_stream_t stream, int32_t stalled_block, uint32_t limit_cycles) {
+    if (stalled_block < 0 || limit_cycles == 0) {
+        g_last_error = "stalled_block must be >= 0 and limit_cycles > 0";
+        return DG_ERR_INVALID_ARG;
+    }
+    return mx4_matmul_impl(a, a_scales, w, w_scales, M, N, K, out, out_dtype, stream, stalled_block, static_cast<long long>(limit_cycles));
 }
 
 size_t dg_ffw_mx4_workspace_size(int32_t rows, int32_t d, int32_t d_ff) {
@@ -1077,6 +1099,32 @@ int dg_sampler_selfcond_step(const void* logits, int logits_dtype, int64_t ld, c
                          z_workspace_bytes, stream, -1, 0, true, false);
 }
 
+
+int dg_test_block_norm_stall(const void* x, int act_dtype, const void* w_pre, int param_dtype, int32_t rows, int32_t d, void* h,
+                             uint32_t limit_cycles, dg_stream_t stream) {
+    g_last_error.clear();
+    int rc;
+    if (limit_cycles == 0) return fail(DG_ERR_INVALID_ARG, "limit_cycles must be > 0");
+    if ((rc = check_norm_shape(act_dtype, param_dtype, 1, rows, d, 1.0f)) != DG_OK) return rc;
+    if (!x || !w_pre || !h) return fail(DG_ERR_INVALID_ARG, "x, w_pre and h are required");
+    if ((rc = check_norm_rows("x", x, d, act_dtype, d)) != DG_OK) return rc;
+    if (!aligned16(w_pre) || !aligned16(h)) return fail(DG_ERR_ALIGNMENT, "w_pre and h must be 16-byte aligned");
+    if ((rc = check_device()) != DG_OK) return rc;
+    BlockNormParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = x;
+    p.ld_x = d;
+    p.w_pre = w_pre;
+    p.R = p.C = rows;
+    p.d = d;
+    p.res_scale = 1.0f;
+    p.eps = 1e-6f;
+    p.h = h;
+    p.wait_limit = static_cast<long long>(limit_cycles);
+    const cudaError_t e = launch_block_norm(p, act_dtype == DG_BF16, param_dtype == DG_BF16, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "block norm stall test launch");
+    return DG_OK;
+}
 
 int dg_test_merge_stall(const void* logits, int logits_dtype, int64_t ld, int32_t rows, int32_t V, float* lse,
                         void* workspace, size_t workspace_bytes, uint32_t limit_cycles, dg_stream_t stream) {

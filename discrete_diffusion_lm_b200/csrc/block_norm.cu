@@ -272,25 +272,25 @@ struct Rings {
     WaitCtl wc;
 };
 template <int kGroups>
-__device__ __forceinline__ void rings_init(Rings<kGroups>& rings) {
+__device__ __forceinline__ void rings_init(Rings<kGroups>& rings, long long wait_limit) {
     if (threadIdx.x == 0) {
         for (int g = 0; g < kGroups; ++g)
             for (int s = 0; s < kMaxSlots; ++s) mbar_init(&rings.full[g][s], 1);
         rings.wc.abort = 0;
-        rings.wc.limit = kWaitLimitCycles;
+        rings.wc.limit = wait_limit > 0 ? wait_limit : kWaitLimitCycles;
         fence_barrier_init();
     }
     __syncthreads();
 }
-// A row that never arrives: the error is recorded and the walk goes on (its waits end at once), so
-// that every thread keeps to the same barriers.  Copies still in flight are waited for at the end.
+// A row that never arrives: the error is recorded, nothing more is fetched, and the walk goes on (its
+// waits end at once), so that every thread keeps to the same barriers.  At the end the threads that
+// fill slots wait for the last copy that each has issued.
 template <int kGroups>
-__device__ __forceinline__ void rings_drain(Rings<kGroups>& rings, int group, bool leader, int rows, int slots) {
-    if (leader && aborted(&rings.wc)) {
+__device__ __forceinline__ void rings_drain(Rings<kGroups>& rings, int group, int slot, int fills) {
+    if (fills > 0 && aborted(&rings.wc)) {
         const long long t0 = clock64();
-        for (int i = max(0, rows - slots); i < rows; ++i)
-            while (!mbar_try_wait(&rings.full[group][i % slots], (i / slots) & 1) && clock64() - t0 < rings.wc.limit) {
-            }
+        while (!mbar_try_wait(&rings.full[group][slot], (fills - 1) & 1) && clock64() - t0 < rings.wc.limit) {
+        }
     }
     __syncthreads();
 }
@@ -396,11 +396,13 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
     const int r0 = static_cast<int>(min(first, static_cast<int64_t>(p.R))), n = min(run, p.R - r0);
     const float inv_d = 1.0f / static_cast<float>(d);
     uint8_t* ring = slots_mem + group * slots * slot_bytes;
-    rings_init(rings);
+    rings_init(rings, p.wait_limit);
     const int ahead = min(n, slots);  // rows fetched before the walk; slot s is always filled by thread s
     const T* next_x = static_cast<const T*>(p.x) + (static_cast<int64_t>(r0) + (t < ahead ? t : 0)) * p.ld_x;
     const T* next_y = static_cast<const T*>(p.y) + (static_cast<int64_t>(r0) + (t < ahead ? t : 0)) * p.ld_y;
+    int fills = 0;
     const auto fetch = [&](int slot) {  // the next row, into a free slot
+        if (aborted(&rings.wc)) return;
         uint64_t* bar = &rings.full[group][slot];
         uint8_t* dst = ring + slot * slot_bytes;
         mbar_arrive_expect_tx(bar, slot_bytes);
@@ -408,8 +410,9 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
         if (post) bulk_load(dst + row_bytes, next_y, row_bytes, bar);
         next_x += slots * p.ld_x;
         next_y += slots * p.ld_y;
+        ++fills;
     };
-    if (t < ahead) fetch(t);
+    if (t < ahead && !(p.wait_limit > 0 && r0 == 0 && t == 0)) fetch(t);  // (the test hook leaves row 0 out)
     Pair wc[kNV][kP], wpre[kNV][kP];  // res_scale gate w_post, w_pre
     int canvas = r0 / p.C, left = 0;  // rows before wc is of the next canvas
     const auto load_post = [&]() {
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
             phase ^= 1;
         }
     }
-    rings_drain(rings, group, t == 0, n, slots);
+    rings_drain(rings, group, t, fills);
 }
 
 // kCtas CTAs per SM share its shared memory.
@@ -692,10 +695,12 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
     const uint32_t at_h = up ? row_bytes : 0, at_x = at_h + (pre ? row_bytes : 0), at_y = at_x + (pre ? row_bytes : 0);
     const uint32_t slot_bytes = at_y + (post ? row_bytes : 0);
     uint8_t* ring = slots_mem + group * slots * slot_bytes;
-    rings_init(rings);
+    rings_init(rings, p.wait_limit);
     const int ahead = min(n, slots);  // rows fetched before the walk; slot s is always filled by thread s
     int64_t next = r0 + (t < ahead ? t : 0) * kGroups;
+    int fills = 0;
     const auto fetch = [&](int slot) {  // the next row, into a free slot
+        if (aborted(&rings.wc)) return;
         uint64_t* bar = &rings.full[group][slot];
         uint8_t* dst = ring + slot * slot_bytes;
         mbar_arrive_expect_tx(bar, slot_bytes);
@@ -706,6 +711,7 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
         }
         if (post) bulk_load(dst + at_y, static_cast<const T*>(p.y) + next * p.ld_y, row_bytes, bar);
         next += slots * kGroups;
+        ++fills;
     };
     if (t < ahead) fetch(t);
     Pair wp[kNV][kP], wc[kNV][kP], acc_pre[kNV][kP], acc_post[kNV][kP];
@@ -804,7 +810,7 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
             phase ^= 1;
         }
     }
-    rings_drain(rings, group, t == 0, n, slots);
+    rings_drain(rings, group, t, fills);
     grid_launch_dependents();
     // the groups' sums, by way of the ring's memory: group 0 adds the others' to its own
     for (int which = 0; which < 2; ++which) {

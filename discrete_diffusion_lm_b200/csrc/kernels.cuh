@@ -151,6 +151,7 @@ struct BlockNormParams {
     float res_scale, eps;
     void *x_out, *h;        // [R, d]
     float *rstd_y, *rstd_x;  // [R] or null
+    long long wait_limit;    // test hook: cycles a wait may last, and row 0 is never fetched (0: the default)
 };
 cudaError_t launch_block_norm(const BlockNormParams& p, int act_bf16, int param_bf16, cudaStream_t s);
 
@@ -165,6 +166,7 @@ struct BlockNormBackwardParams {
     void *dx, *dy;             // [R, d]
     float *dw_post, *dgate, *dw_pre;
     float *part_pre, *part_post;  // [B * runs, d] partial sums
+    long long wait_limit;         // cycles a wait may last (0: the default)
 };
 int32_t block_norm_runs(int32_t B, int32_t C, int32_t d, int act_bf16);
 cudaError_t launch_block_norm_backward(const BlockNormBackwardParams& p, int act_bf16, int param_bf16, cudaStream_t s);
@@ -191,6 +193,8 @@ struct Mx4MatmulParams {
     void* out;            // [M, N] bf16 or fp32, or codes [M, N / 2]
     uint8_t* out_scales;  // kMx4OutGelu
     int32_t dependent;    // 1: launch as a programmatic dependent of the kernel that writes a
+    long long wait_limit;  // test hook: cycles a wait may last (0: the default) ...
+    int32_t fault_block;   // ... and the 256-value block of K whose copies are then never issued
 };
 cudaError_t launch_mx4_matmul(const Mx4MatmulParams& p, cudaStream_t s);
 cudaError_t read_and_clear_mx4_error(int* out);

@@ -217,6 +217,7 @@ struct alignas(64) Mx4Kernel {
     int32_t M, N, K;
     int32_t n_tiles, k_tiles, k_blocks;  // 128-column tiles; 128-value and 256-value steps of K
     long long wait_limit;
+    int32_t fault_block;  // test hook: W's copies of this 256-value block are never issued (-1: none)
 };
 
 // kind::mxf4 instruction descriptor: E2M1 operands (type 1), E8M0 scales, M = 128, N = 128; the scale
@@ -383,12 +384,13 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid
                 phase ^= 1;
             }
             if (!mbar_wait(&empty[s], phase ^ 1, wc)) break;
-            load_stage(kb, s++, is_a);
+            if (is_a || kb != p.fault_block) load_stage(kb, s, is_a);
+            ++s;
         }
         if (aborted(wc)) {  // let the copies in flight land before the shared memory goes away
             const long long t0 = clock64();
-            for (int i = max(0, kb - kb0 - stages); i < kb - kb0; ++i)
-                while (!mbar_try_wait(&full[i % stages], (i / stages) & 1) && clock64() - t0 < wc->limit) {
+            for (int i = max(0, kb - kb0 - stages); i < kb - kb0; ++i)  // (a block left out by the test hook never lands)
+                while (kb0 + i != p.fault_block && !mbar_try_wait(&full[i % stages], (i / stages) & 1) && clock64() - t0 < wc->limit) {
                 }
         }
     } else if (warp == 1) {
@@ -509,7 +511,13 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid
             }
         }
         __syncwarp();
-        if (rows > 0) ok = mbar_wait(inbox_full, 0, wc) && ok;
+        if (rows > 0 && !mbar_wait(inbox_full, 0, wc)) {
+            // given up elsewhere in this CTA: the other splits' shares are under way all the same
+            const long long t0 = clock64();
+            while (!mbar_try_wait(inbox_full, 0) && clock64() - t0 < wc->limit) {
+            }
+            ok = false;
+        }
         ok = __syncthreads_and(ok);
         cluster_arrive();  // every share sent to this CTA is here
     }
@@ -636,6 +644,7 @@ struct alignas(64) Mx4PairKernel {
     int32_t M, N, K;
     int32_t m_tiles, n_tiles, k_tiles, k_blocks;
     long long wait_limit;
+    int32_t fault_block;  // test hook: the copies of this block are never issued (-1: none)
 };
 
 template <int kN>
@@ -728,6 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const int s = i % G::kStages;
                 ok = mbar_wait(&empty[s], ((i / G::kStages) & 1) ^ 1, wc);
                 if (!ok) break;
+                if (kb == p.fault_block) continue;
                 if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * G::kStage);
                 uint8_t* st = smem + s * G::kStage;
                 const uint32_t bar = leader_full + s * 8;
@@ -743,7 +753,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (aborted(wc) && rank == 0) {  // copies in flight land on the leader's barriers: wait for them (bounded)
             const long long t0 = clock64();
             for (int k = max(0, i - G::kStages); k < i; ++k)
-                while (!mbar_try_wait(&full[k % G::kStages], (k / G::kStages) & 1) && clock64() - t0 < wc->limit) {
+                while (k % p.k_blocks != p.fault_block && !mbar_try_wait(&full[k % G::kStages], (k / G::kStages) & 1) && clock64() - t0 < wc->limit) {
                 }
         }
     } else if (warp == 1 && rank == 0) {
@@ -962,7 +972,8 @@ cudaError_t launch_pair(const Mx4MatmulParams& q, cudaStream_t st) {
     kp.n_tiles = (q.N + kN - 1) / kN;
     kp.k_tiles = (q.K + 127) / 128;
     kp.k_blocks = (q.K + kKStage - 1) / kKStage;
-    kp.wait_limit = kWaitLimitCycles;
+    kp.wait_limit = q.wait_limit > 0 ? q.wait_limit : kWaitLimitCycles;
+    kp.fault_block = q.wait_limit > 0 ? q.fault_block : -1;
     kp.out_codes = static_cast<uint8_t*>(q.out);
     kp.out_scales = q.out_scales;
     const uint64_t ta = static_cast<uint64_t>((q.M + 127) / 128) * kp.k_tiles, tw = static_cast<uint64_t>((q.N + 127) / 128) * kp.k_tiles;
@@ -1063,7 +1074,8 @@ cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
     kp.n_tiles = (q.N + kNTile - 1) / kNTile;
     kp.k_tiles = (q.K + 127) / 128;
     kp.k_blocks = k_blocks;
-    kp.wait_limit = kWaitLimitCycles;
+    kp.wait_limit = q.wait_limit > 0 ? q.wait_limit : kWaitLimitCycles;
+    kp.fault_block = q.wait_limit > 0 ? q.fault_block : -1;
     const int64_t grid = singles * splits;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (q.out_kind == kMx4OutF32) return launch_product<kOutF32>(kp, static_cast<int>(grid), splits, q.dependent != 0, st);
