@@ -657,6 +657,8 @@ class _On:
     """The device and stream that a call runs on, where they are not the current ones."""
 
     def __init__(self, dev: int, stream):
+        if stream is not None and stream.device_index != dev:
+            raise ValueError(f"the stream is on device {stream.device_index}, the tensors are on device {dev}")
         self.parts = [torch.cuda.device(dev)] + ([torch.cuda.stream(stream)] if stream is not None else [])
 
     def __enter__(self):
@@ -685,7 +687,7 @@ def dg_block_norm(x: torch.Tensor, w_pre: Optional[torch.Tensor] = None, *, y: O
         raise ValueError("x must be a 2-D tensor")
     R, d = shape
     px, ld_x = _rows_arg(x, "x", dev, dtype, shape)
-    C = R if C is None else C
+    C = R if C is None or gate is None else C  # without a gate rows need no grouping
     if C < 1 or R % C:
         raise ValueError("rows must be a multiple of C")
     given = w_pre if w_pre is not None else w_post
@@ -746,7 +748,7 @@ def dg_block_norm_backward(dx_out: Optional[torch.Tensor], dh: Optional[torch.Te
     if len(shape) != 2:
         raise ValueError("x must be a 2-D tensor")
     R, d = shape
-    C = R if C is None else C
+    C = R if C is None or gate is None else C  # without a gate rows need no grouping
     if C < 1 or R % C:
         raise ValueError("rows must be a multiple of C")
     given = w_pre if w_pre is not None else w_post

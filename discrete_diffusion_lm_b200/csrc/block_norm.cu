@@ -508,11 +508,8 @@ cudaError_t launch_rows_as(const BlockNormParams& p, cudaStream_t st) {
     const int64_t groups = static_cast<int64_t>(kCtas) * num_sms() * kGroups;
     const int run = static_cast<int>((p.R + groups - 1) / groups);
     const int64_t ctas = (p.R + static_cast<int64_t>(run) * kGroups - 1) / (static_cast<int64_t>(run) * kGroups);
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(block_norm_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-    });
+    static DeviceOnce once;
+    const cudaError_t attr_err = allow_shared_memory(once, block_norm_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull>, kRingBytes);
     if (attr_err != cudaSuccess) return attr_err;
     block_norm_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull><<<static_cast<unsigned>(ctas), 32 * kW * kGroups, kGroups * slots * slot, st>>>(p, slots, run);
     note_launches(1);
@@ -769,10 +766,10 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
             read(k, g, h, x, y);
 #pragma unroll
             for (int j = 0; j < kP; ++j) {
-                const Pair tt = mul2(h[j], wp[k][j]), cy = mul2(wc[k][j], y[j]);
-                sum0 = fma2(tt, x[j], sum0);
-                sum1 = fma2(cy, fma2(rx2, tt, g[j]), sum1);
-                sum2_ = fma2(cy, x[j], sum2_);
+                const Pair m = mul2(x[j], rx2), tt = mul2(h[j], wp[k][j]), cv = mul2(wc[k][j], mul2(y[j], ry2));
+                sum0 = fma2(tt, m, sum0);
+                sum1 = fma2(cv, fma2(rx2, tt, g[j]), sum1);
+                sum2_ = fma2(cv, m, sum2_);
             }
         }
         float s[3] = {sum2(sum0), sum2(sum1), sum2(sum2_)};
@@ -781,9 +778,7 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
         // past this barrier every thread is done with the row before: its slot is free
         const int before = slot == 0 ? slots - 1 : slot - 1;
         if (t == before && i > 0 && i - 1 + slots < n) fetch(before);
-        // sums of t x, c y (dx' + rstd_x t), c y x: the means' rstd factors are put in here
-        const float m1 = rx * s[0] * inv_d, m2 = ry * fmaf(-rx * rx * m1, s[2], s[1]) * inv_d;
-        const float a = -rx * rx * m1, e = -ry * ry * m2;
+        const float a = -rx * s[0] * inv_d, e = -ry * fmaf(a, s[2], s[1]) * inv_d;
         const Pair a2 = pair(a, a), e2 = pair(e, e);
 #pragma unroll
         for (int k = 0; k < kNV; ++k) {
@@ -793,11 +788,11 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
                 read(k, g, h, x, y);
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
-                    dx[j] = fma2(a2, x[j], fma2(rx2, mul2(h[j], wp[k][j]), g[j]));
-                    acc_pre[k][j] = fma2(mul2(h[j], rx2), x[j], acc_pre[k][j]);
-                    const Pair u = mul2(dx[j], ry2);
-                    acc_post[k][j] = fma2(u, y[j], acc_post[k][j]);
-                    dy[j] = fma2(e2, y[j], mul2(wc[k][j], u));
+                    const Pair m = mul2(x[j], rx2), v = mul2(y[j], ry2);
+                    dx[j] = fma2(a2, m, fma2(rx2, mul2(h[j], wp[k][j]), g[j]));
+                    acc_pre[k][j] = fma2(h[j], m, acc_pre[k][j]);
+                    acc_post[k][j] = fma2(dx[j], v, acc_post[k][j]);
+                    dy[j] = fma2(e2, v, mul2(wc[k][j], mul2(dx[j], ry2)));
                 }
                 *reinterpret_cast<uint4*>(dxo + k * (kN * kThreads)) = pack_pairs<T>(dx);
                 if (post) *reinterpret_cast<uint4*>(dyo + k * (kN * kThreads)) = pack_pairs<T>(dy);
@@ -946,11 +941,8 @@ cudaError_t launch_backward_rows_as(const BlockNormBackwardParams& p, cudaStream
     const int slot = p.d * static_cast<int>(sizeof(T)) * ((p.dx_out ? 1 : 0) + (p.w_pre ? 2 : 0) + (p.y ? 1 : 0));
     const int slots = std::min(kMaxSlots, kRingBytes / (slot * kGroups));
     const int bytes = std::max(kGroups * slots * slot, (kGroups - 1) * p.d * 4);
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(block_norm_backward_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-    });
+    static DeviceOnce once;
+    const cudaError_t attr_err = allow_shared_memory(once, block_norm_backward_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull>, kRingBytes);
     if (attr_err != cudaSuccess) return attr_err;
     block_norm_backward_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull><<<static_cast<unsigned>(p.B) * p.runs, 32 * kW * kGroups, bytes, st>>>(p, slots);
     return launch_params<P>(p, st);

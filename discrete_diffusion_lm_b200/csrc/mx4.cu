@@ -581,11 +581,8 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid
 
 template <int kOut, bool kFew = false>
 cudaError_t launch_product(const Mx4Kernel& kp, int grid, int splits, bool dependent, cudaStream_t st) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(mx4_matmul_kernel<kOut, kFew>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMx4Smem));
-    });
+    static DeviceOnce once;
+    const cudaError_t attr_err = allow_shared_memory(once, mx4_matmul_kernel<kOut, kFew>, static_cast<int>(kMx4Smem));
     if (attr_err != cudaSuccess) return attr_err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -957,11 +954,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 template <int kOut, int kN>
 cudaError_t launch_pair(const Mx4MatmulParams& q, cudaStream_t st) {
     using G = PairTile<kN>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(mx4_matmul_pair_kernel<kOut, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(G::kSmem));
-    });
+    static DeviceOnce once;
+    const cudaError_t attr_err = allow_shared_memory(once, mx4_matmul_pair_kernel<kOut, kN>, static_cast<int>(G::kSmem));
     if (attr_err != cudaSuccess) return attr_err;
     Mx4PairKernel kp;
     std::memset(&kp, 0, sizeof(kp));

@@ -339,7 +339,8 @@ int dg_ffw(const void* z_in, int32_t rows, int32_t d, int32_t d_ff, const void* 
 /* where ld_x = d; otherwise no output aliases an input or another output.  */
 /* rstd_y, rstd_x: device float [B*C], the reciprocal root means that the   */
 /* backward pass takes, or NULL.                                             */
-/* d is a multiple of 8 in [8, 16384]; 1 <= B <= DG_MAX_CANVASES, C >= 1,   */
+/* d is a multiple of 8 in [8, 16384]; 1 <= B <= DG_MAX_CANVASES (without a */
+/* gate B = 1, C = rows will do for any number of rows), C >= 1,            */
 /* B*C < 2^31; eps >= 0.  One launch, no workspace.                         */
 /* ------------------------------------------------------------------------ */
 int dg_block_norm(const void* x, int64_t ld_x, const void* y, int64_t ld_y, int act_dtype,
@@ -398,7 +399,8 @@ int dg_block_norm_backward(const void* dx_out, int64_t ld_dx_out, const void* dh
 /* dg_mx4_dequantize: the values, as DG_F32 (exact; subnormal results are    */
 /*   kept) or DG_BF16 (exact except where 2^(c-127) leaves its range) in out */
 /*   [rows, K], contiguous.                                                  */
-/* All pointers 16-byte aligned, nothing aliased, no workspace, one launch.  */
+/* K <= 2^24, rows <= 2^31 - 256.  All pointers 16-byte aligned, nothing      */
+/* aliased, no workspace, one launch.                                        */
 /* ------------------------------------------------------------------------ */
 size_t dg_mx4_scale_bytes(int32_t rows, int32_t K);
 

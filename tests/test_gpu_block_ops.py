@@ -17,6 +17,8 @@ Tolerances, from the arithmetic (U = 2^-24 is half a step of fp32, S half a step
     its block's largest magnitude across a power of two, the value may be off by the spacing there.
 """
 import math
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -91,13 +93,33 @@ def test_norm_forward(B, C, d, T, P):
         check_forward(x, y, w_post, gate, w_pre, C, s, torch.tensor(1e-6, dtype=F32).item(), out)
 
 
+# many rows: the form that keeps rows in flight, its widths full and not, canvases that end inside a
+# CTA's run of rows
+MANY = [(3, 500, 64), (256, 5, 72), (5, 300, 256), (4, 400, 512), (3, 401, 1000), (2, 700, 1024), (2, 700, 2048), (7, 200, 2056),
+        (2, 600, 4096), (3, 397, 5000), (1, 1200, 8192), (7, 171, 8200)]
+
+
+@pytest.mark.parametrize("T,P", [(BF16, BF16), (BF16, F32), (F32, F32)])
+@pytest.mark.parametrize("B,C,d", MANY)
+def test_norm_forward_many_rows(B, C, d, T, P):
+    s, eps = torch.tensor(0.7, dtype=F32).item(), torch.tensor(1e-6, dtype=F32).item()
+    for mode, gated in (("both", True), ("both", False), ("pre", False), ("post", True)):
+        x, y, w_post, gate, w_pre = norm_inputs(B, C, d, T, P, mode, gated)
+        out = dg.dg_block_norm(x, w_pre, y=y, w_post=w_post, gate=gate, C=C, res_scale=0.7, eps=1e-6)
+        check_forward(x, y, w_post, gate, w_pre, C, s, eps, out)
+    assert dg.dg_device_error() == 0
+
+
+@pytest.mark.parametrize("rows", [4, 500])
 @pytest.mark.parametrize("T", [BF16, F32])
-def test_norm_strided_rows_and_in_place_stream(T):
+def test_norm_strided_rows_and_in_place_stream(T, rows):
     g = gen(3)
-    big, C, d = randn(g, 12, 3 * 328, dtype=T), 3, 320
+    big, C, d = randn(g, 3 * rows, 3 * 328, dtype=T), 3, 320
+    _, _, w_post, gate, w_pre = norm_inputs(4, 3, d, T, F32, "both", True)
+    if rows > 4:
+        C = 3 * rows // 4
     x, y = big[:, 8:8 + d], big[:, 400:400 + d]
     assert x.stride(0) == 984 and x.data_ptr() % 16 == 0
-    _, _, w_post, gate, w_pre = norm_inputs(4, 3, d, T, F32, "both", True)
     kept = big.clone()
     out = dg.dg_block_norm(x, w_pre, y=y, w_post=w_post, gate=gate, C=C, res_scale=-1.5)
     check_forward(x, y, w_post, gate, w_pre, C, -1.5, torch.tensor(1e-6, dtype=F32).item(), out)
@@ -122,6 +144,21 @@ def test_norm_zero_rows_nan_rows_and_wide_values():
         within(out["h"][r], ref.norm_rows(x[r:r + 1], 0.0)[0], 48 * U * 4, f"row {r}")
     assert dg.dg_block_norm(x[:1], w, eps=1e-6)["h"].abs().max().item() == 0.0
     within(dg.dg_block_norm(x[4:5], w, eps=1e-6)["h"], x[4:5].double() * 1e3, 1e-6 * 1e-22, "tiny row")
+
+
+@pytest.mark.parametrize("rows", [12, 1500])
+def test_norm_rows_beyond_the_squares_range(rows):
+    # rows of 1e-25 and 1e25: their squares leave fp32, and every result but rstd is as at any size
+    d, C = 512, rows
+    x, y, w_post, _, w_pre = norm_inputs(1, C, d, F32, F32, "both", False)
+    size = torch.tensor([1.0, 1e-25, 1e25], device=DEV).repeat(rows // 3)[:, None]
+    x, y = x * size, y * size.flip(0)
+    out = dg.dg_block_norm(x, w_pre, y=y, w_post=w_post, eps=0.0)
+    check_forward(x, y, w_post, None, w_pre, C, 1.0, 0.0, out)
+    g = gen(3)
+    dxo, dh = randn(g, rows, d), randn(g, rows, d)
+    res = dg.dg_block_norm_backward(dxo, dh, out["x"], w_pre, rstd_x=out["rstd_x"], y=y, w_post=w_post, rstd_y=out["rstd_y"])
+    check_backward((dxo, dh, out["x"], w_pre, out["rstd_x"], y, w_post, None, out["rstd_y"]), C, 1.0, res, F32)
 
 
 # ------------------------------------------------------------------------------------ norms, backward
@@ -367,6 +404,19 @@ def test_block(R, d, dff):
     assert torch.equal(dg.dg_ffw_mx4(zin, w1, w2, out=zin), got)
 
 
+@pytest.mark.parametrize("R", [8, 200])
+def test_block_nan_and_infinite_rows_stay_alone(R):
+    g = gen(13)
+    z = randn(g, R, 128, dtype=BF16)
+    w1, w2 = dg.dg_mx4_quantize(randn(g, 256, 128, std=0.1)), dg.dg_mx4_quantize(randn(g, 128, 256, std=0.1))
+    clean = dg.dg_ffw_mx4(z, w1, w2)
+    z[3, 5], z[6, 100] = float("nan"), float("-inf")
+    got = dg.dg_ffw_mx4(z, w1, w2)
+    keep = torch.ones(R, dtype=torch.bool, device=DEV)
+    keep[3] = keep[6] = False
+    assert got[~keep].isnan().all() and torch.equal(got[keep], clean[keep])
+
+
 def test_block_is_its_parts_up_to_the_hidden_rounding():
     # against the bf16 block on the same (dequantised) weights: 4-bit rounding of the input and of the
     # hidden layer is the only difference, each about 10 % of a value, so the results are strongly alike
@@ -461,6 +511,52 @@ def test_other_stream_two_streams_and_graphs():
             assert torch.equal(outs[k][0], ye)
             assert all(torch.equal(outs[k][1][n], oe[n]) for n in oe) and all(torch.equal(outs[k][2][n], be[n]) for n in be)
     assert dg.dg_device_error() == 0
+
+
+def test_first_call_of_a_process_may_be_captured():
+    # nothing that a first call sets up needs a call outside of a capture
+    code = """
+import torch, discrete_diffusion_lm_b200 as dg
+z = torch.randn(200, 2048, device='cuda').bfloat16(); big = torch.randn(2000, 2048, device='cuda').bfloat16()
+w = torch.ones(2048, device='cuda'); q = torch.zeros(2048, 1024, dtype=torch.uint8, device='cuda'); s = torch.full((16, 16, 32, 16), 127, dtype=torch.uint8, device='cuda')
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a = dg.dg_block_norm(big, w); y = dg.dg_ffw_mx4(z, (q, s), (q, s)); o = dg.dg_ffw_mx4(big, (q, s), (q, s))
+    b = dg.dg_block_norm_backward(None, big, big, w, rstd_x=a['rstd_x'])
+g.replay(); torch.cuda.synchronize()
+assert dg.dg_device_error() == 0 and y.abs().max().item() == 0 and torch.equal(a['h'], dg.dg_block_norm(big, w)['h'])
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
+
+
+def test_offsets_beyond_32_bits():
+    # the last rows of arrays of more than 2^31 elements
+    rows, d = 300_000, 8192
+    x = torch.zeros(rows, d, dtype=BF16, device=DEV)
+    x[-3:] = randn(gen(30), 3, d, dtype=BF16)
+    w = torch.ones(d, dtype=BF16, device=DEV)
+    out = dg.dg_block_norm(x, w)
+    assert torch.equal(out["h"][-3:], dg.dg_block_norm(x[-3:].contiguous(), w)["h"]) and out["h"][:-3].abs().max().item() == 0
+    res = dg.dg_block_norm_backward(None, x, x, w, rstd_x=out["rstd_x"])
+    small = dg.dg_block_norm_backward(None, x[-3:].contiguous(), x[-3:].contiguous(), w, rstd_x=out["rstd_x"][-3:].contiguous())
+    assert torch.equal(res["dx"][-3:], small["dx"])
+    del out, res
+    codes, scales = dg.dg_mx4_quantize(x)
+    want = dg.dg_mx4_quantize(x[-3:].contiguous())
+    r = torch.arange(rows - 3, rows, device=DEV)
+    assert torch.equal(codes[-3:], want[0])
+    assert torch.equal(ref.mx4_unpack(codes[-3:], dg.dg_mx4_quantize(x[-3:].contiguous())[1])[1], scales[r // 128, :, r % 32].reshape(3, d // 128, 4, 4)[
+        torch.arange(3, device=DEV), :, r // 32 % 4].reshape(3, d // 32).long())
+    back = dg.dg_mx4_dequantize(codes, scales)
+    assert torch.equal(back[-3:], dg.dg_mx4_dequantize(*want))
+    del x, back, codes, scales
+    g = gen(31)
+    M, N = 70_000, 32_768
+    (a, av), (w2, wv) = random_mx4(g, M, 32), random_mx4(g, N, 32)
+    out = dg.dg_mx4_matmul(a, w2)
+    want = av[-2:] @ wv.T
+    within(out[-2:], want, 130 * U * (av[-2:].abs() @ wv.abs().T) + half_step(BF16) * want.abs(), "last rows")
 
 
 def test_launch_counts():
