@@ -214,28 +214,6 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) block_norm_ke
 // walk, so the parameters stay in registers, as fp32 pairs for the packed fma.rn.f32x2, and widths
 // that fill every thread's vectors (kFull) have no column checks.  A CTA has kGroups groups, each with
 // its own ring and named barrier.
-using Pair = unsigned long long;  // two fp32 values
-__device__ __forceinline__ Pair pair(float lo, float hi) {
-    Pair p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
-    return p;
-}
-__device__ __forceinline__ void unpair(Pair p, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    Pair d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ float sum2(Pair p) {
-    float a, b;
-    unpair(p, a, b);
-    return a + b;
-}
 template <typename T, int kP>
 __device__ __forceinline__ void unpack_pairs(const uint4& v, Pair (&p)[kP]) {
     float f[2 * kP];

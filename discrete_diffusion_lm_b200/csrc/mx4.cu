@@ -265,19 +265,25 @@ __device__ __forceinline__ uint32_t cluster_size() {
     return r;
 }
 
-// GELU, tanh form, as x / (1 + exp(-2u)): the hidden layer is rounded to 4 bits by comparisons with
-// the E2M1 midpoints, so an error here moves values across them; the hardware tanh's 2^-11 would
-// move one value in a few hundred, ex2 and a reciprocal (about 2^-22) one in a million.  u is kept
-// below 2^7, where the quotient is under 2^-100 and the reciprocal still a normal number.
+// GELU, tanh form, as x / (1 + exp(-2u)), two values at a time.  The hidden layer is rounded to 4 bits
+// by comparisons with the E2M1 midpoints, so an error here moves values across them: the hardware
+// tanh's 2^-11 would move one value in a few hundred, ex2 and a reciprocal (about 2^-22) one in a
+// million.  u is kept below 2^7, where the quotient is 2^-125 x and the reciprocal still a normal number.
+// (A reciprocal by Newton's iteration, off the special-function unit, was no faster: the epilogue's
+// 6000 cycles a tile are beside the products' 5700 already.)
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float gelu_exact(float x) {
+__device__ __forceinline__ Pair gelu_pair(Pair x) {
     const float k0 = -2.0f * 0.7978845608028654f * kLog2e;  // -2 sqrt(2 / pi) log2 e
-    const float u = x * fmaf(k0 * 0.044715f, x * x, k0);
-    return x * rcp_approx(1.0f + ex2_approx(fminf(u, 125.0f)));
+    const float k1 = k0 * 0.044715f;
+    float lo, hi;
+    unpair(mul2(x, fma2(mul2(x, x), pair(k1, k1), pair(k0, k0))), lo, hi);
+    lo = rcp_approx(1.0f + ex2_approx(fminf(lo, 125.0f)));
+    hi = rcp_approx(1.0f + ex2_approx(fminf(hi, 125.0f)));
+    return mul2(x, pair(lo, hi));
 }
 // max(a, |b|) that keeps a NaN.
 __device__ __forceinline__ float max_abs_nan(float a, float b) {
@@ -553,7 +559,9 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid
                         make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
             } else {
                 // eight lanes hold a block of 32 hidden values
-                const float f[4] = {gelu_exact(v.x), gelu_exact(v.y), gelu_exact(v.z), gelu_exact(v.w)};
+                float f[4];
+                unpair(gelu_pair(pair(v.x, v.y)), f[0], f[1]);
+                unpair(gelu_pair(pair(v.z, v.w)), f[2], f[3]);
                 uint32_t top = __float_as_uint(max_abs_nan(max_abs_nan(max_abs_nan(fabsf(f[0]), f[1]), f[2]), f[3]));
 #pragma unroll
                 for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -862,9 +870,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const uint32_t* v = all + c;
                     float f[32], most[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) {
-                        f[q] = gelu_exact(__uint_as_float(v[q]));
+                    for (int q = 0; q < 32; q += 2) {
+                        unpair(gelu_pair(pair(__uint_as_float(v[q]), __uint_as_float(v[q + 1]))), f[q], f[q + 1]);
                         most[q & 3] = max_abs_nan(most[q & 3], f[q]);
+                        most[(q & 3) + 1] = max_abs_nan(most[(q & 3) + 1], f[q + 1]);
                     }
                     const uint32_t top = __float_as_uint(max_abs_nan(max_abs_nan(most[0], most[1]), max_abs_nan(most[2], most[3])));
                     const bool in = valid && col0 + c < p.N;
@@ -1030,12 +1039,11 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
 }
 
 cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
-    // Which kernel, from sizes alone (measured in us, us a product, K = 2048 unless said):
+    // Which kernel, from sizes alone (us a product, K = 2048 unless said):
     //  * up to 128 rows half of a pair's tile would be empty: single CTAs, K split;
-    //  * more 256 x 128 tiles than pairs: 256 x 256 tiles (96 tiles: 9.0, with 128 columns 10.2, single
-    //    CTAs 14.7) - but 256 x 128 where the epilogue is the longer part (gelu on 4096 x 4096 x 1024:
-    //    block 35.5, with 256 columns 39.7);
-    //  * fewer: 256 x 128 tiles (64 tiles: 7.4, single CTAs 8.2; 8 tiles: 7.0 and 6.9), unless splitting K
+    //  * more 256 x 128 tiles than pairs: 256 x 256 tiles (96 tiles: 8.6, with 128 columns 10.2, single
+    //    CTAs 14.7; a block on 4096 rows of 2048: 70, with 128 columns 83);
+    //  * fewer: 256 x 128 tiles (64 tiles: 7.0, single CTAs 8.2; 8 tiles: 6.5 and 6.9), unless splitting K
     //    makes up for it, which takes K > 2048 (32 tiles at K = 8192: 14.9, split in two 12.5).
     const int64_t pairs = static_cast<int64_t>((q.M + 255) / 256) * ((q.N + 127) / 128);
     const int64_t singles = static_cast<int64_t>((q.M + kMTile - 1) / kMTile) * ((q.N + kNTile - 1) / kNTile);
@@ -1048,7 +1056,7 @@ cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
         const bool wide = 2 * pairs > num_sms();
         if (q.out_kind == kMx4OutF32) return wide ? launch_pair<kOutF32, 256>(q, st) : launch_pair<kOutF32, 128>(q, st);
         if (q.out_kind == kMx4OutBf16) return wide ? launch_pair<kOutBf16, 256>(q, st) : launch_pair<kOutBf16, 128>(q, st);
-        return launch_pair<kOutGeluMx4, 128>(q, st);
+        return wide ? launch_pair<kOutGeluMx4, 256>(q, st) : launch_pair<kOutGeluMx4, 128>(q, st);
     }
     Mx4Kernel kp;
     std::memset(&kp, 0, sizeof(kp));

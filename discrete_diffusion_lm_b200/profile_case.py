@@ -7,6 +7,9 @@
     python -m discrete_diffusion_lm_b200.profile_case --kernel selfcond_drop --workload train --reps 3
     python -m discrete_diffusion_lm_b200.profile_case --kernel entropy_bounded --workload full --reps 3
     python -m discrete_diffusion_lm_b200.profile_case --kernel ffw --workload full --reps 3
+    python -m discrete_diffusion_lm_b200.profile_case --kernel ffw_mx4 --workload batched --reps 3
+    python -m discrete_diffusion_lm_b200.profile_case --kernel block_norm --workload batched --reps 3
+    python -m discrete_diffusion_lm_b200.profile_case --kernel block_norm_backward --workload train --reps 3
 
 Inputs come from the seeded workload generators; the logits pass that provides lse for the
 contraction runs once before the contraction launches.  Exits non-zero if a kernel reports a
@@ -26,7 +29,8 @@ from discrete_diffusion_lm_b200 import workloads as W
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
     ap.add_argument("--kernel", choices=["sampler_step", "selfcond", "canvas_ce", "forward_noise", "ce_backward",
-                                         "selfcond_drop", "entropy_bounded", "ffw"], required=True)
+                                         "selfcond_drop", "entropy_bounded", "ffw", "ffw_mx4", "block_norm",
+                                         "block_norm_backward"], required=True)
     ap.add_argument("--workload", default="full", choices=sorted(W.SAMPLER_CONFIGS) + ["train"])
     ap.add_argument("--reps", type=int, default=3)
     a = ap.parse_args(argv)
@@ -56,6 +60,25 @@ def main(argv=None) -> int:
         y, hidden = dg.dg_ffw(zf, w1, w2)
         for _ in range(a.reps - 1):
             dg.dg_ffw(zf, w1, w2, hidden=hidden, out=y)
+    elif a.kernel == "ffw_mx4":
+        cfg = W.SAMPLER_CONFIGS[a.workload]
+        zf, w1, w2 = W.make_ffw(cfg, dev)
+        q1, q2 = (dg.dg_mx4_quantize(w.t().contiguous()) for w in (w1, w2))
+        for _ in range(a.reps):
+            dg.dg_ffw_mx4(zf, q1, q2)
+    elif a.kernel in ("block_norm", "block_norm_backward"):
+        # the rows between two blocks: every canvas of the workload, or every row of a training batch
+        cfg = W.TRAIN if a.workload == "train" else W.SAMPLER_CONFIGS[a.workload]
+        B, C, d = (cfg.n_seq, cfg.L, 2048) if a.workload == "train" else (cfg.B, cfg.C, cfg.d)
+        x, y, g1, g2 = (torch.randn(B * C, d, device=dev).to(torch.bfloat16) for _ in range(4))
+        w, gate = torch.ones(d, device=dev), torch.rand(B, d, device=dev)
+        o = dg.dg_block_norm(x, w, y=y, w_post=w, gate=gate, C=C)
+        for _ in range(a.reps):
+            if a.kernel == "block_norm":
+                dg.dg_block_norm(x, w, y=y, w_post=w, gate=gate, C=C)
+            else:
+                dg.dg_block_norm_backward(g1, g2, o["x"], w, rstd_x=o["rstd_x"], y=y, w_post=w, gate=gate,
+                                          rstd_y=o["rstd_y"], C=C)
     elif a.kernel == "entropy_bounded":
         cfg = W.SAMPLER_CONFIGS[a.workload]
         logits = W.make_logits(cfg, dev)
