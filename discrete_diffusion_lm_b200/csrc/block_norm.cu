@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
             left = p.C;
             load_post();
         }
+        DG_CHECK(g_device_error, r0 + i < p.R && (!p.gate || canvas == (r0 + i) / p.C));
         mbar_wait(&rings.full[group][slot], phase, &rings.wc);
         const uint8_t* src = src0 + slot * slot_bytes;
         Pair fx[kNV][kP], fy[kNV][kP];
@@ -725,6 +726,7 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
         rstd_y += kGroups;
         const float rx_next = pre && more ? *rstd_x : 0.f, ry_next = post && more ? *rstd_y : 0.f;
         const Pair rx2 = pair(rx, rx), ry2 = pair(ry, ry);
+        DG_CHECK(g_device_error, (r0 + i * kGroups) / p.C == b && b < p.B);
         mbar_wait(&rings.full[group][slot], phase, &rings.wc);
         const uint8_t* src = src0 + slot * slot_bytes;
         // a vector's columns of the four rows (zero where the call has none)

@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const T* __restrict__
         uint32_t c = kUnitScale;
         if (r < rows && k < K) {  // K is a multiple of 32: a block's lanes agree
             c = scale_byte(top);
+            DG_CHECK(g_device_error, k + kN <= K && ld >= K);
             const auto q = pack_e2m1(f, inverse_scale(c == 255u ? kUnitScale : c));
             using Code = std::remove_const_t<decltype(q)>;
             *reinterpret_cast<Code*>(codes + static_cast<int64_t>(r) * (K / 2) + k / 2) = c == 255u ? Code(0) : q;
@@ -551,6 +552,7 @@ __global__ void __launch_bounds__(kMx4Threads, 1) mx4_matmul_kernel(const __grid
                 }
             }
             const int64_t r = static_cast<int64_t>(mt) * kMTile + i;
+            DG_CHECK(g_device_error, i < kMTile && (i >= m_valid || (r < p.M && share * splits >= m_valid)));
             if (kOut == kOutF32) {
                 if (col < p.N) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + r * p.N + col) = v;
             } else if (kOut == kOutBf16) {
@@ -878,7 +880,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const uint32_t top = __float_as_uint(max_abs_nan(max_abs_nan(most[0], most[1]), max_abs_nan(most[2], most[3])));
                     const bool in = valid && col0 + c < p.N;
                     const uint32_t sb = in ? scale_byte(top) : kUnitScale;
-                    if (in) {
+                    if (in && DG_CHECKED(g_device_error, r < p.M && col0 + c + 32 <= p.N)) {
                         const float inv = inverse_scale(sb == 255u ? 127u : sb);
                         uint32_t q4[4];
 #pragma unroll
@@ -939,6 +941,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (issuer && col0 + s0 < p.N) {
 #pragma unroll 1
                         for (int q = 0; q < 4 && row0 + 32 * q < p.M; ++q) {
+                            if (!DG_CHECKED(g_device_error, col0 + s0 < p.N && row0 + 32 * q < p.M && t < tiles)) continue;
                             tma_store_2d(&p.tm_out, col0 + s0, row0 + 32 * q, area + q * 4096);
                             bulk_commit();
                             bulk_wait_read_all();

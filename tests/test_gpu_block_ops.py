@@ -32,6 +32,12 @@ DEV = "cuda"
 BF16, F32 = torch.bfloat16, torch.float32
 
 
+@pytest.fixture(autouse=True)
+def no_device_error():
+    yield
+    assert dg.dg_device_error() == 0
+
+
 def gen(seed):
     return torch.Generator(device=DEV).manual_seed(seed)
 
