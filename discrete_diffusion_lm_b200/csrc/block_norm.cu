@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
             const int c = t + k * kThreads;
             if (kFull || c < n_vec) {
                 load_pairs(static_cast<const P*>(p.w_post) + c * kN, wc[k]);
-                if (p.gate) {
+                if (p.gate && DG_CHECKED(g_device_error, canvas < p.R / p.C)) {
                     Pair g[kP];
                     load_pairs(static_cast<const P*>(p.gate) + static_cast<int64_t>(canvas) * d + c * kN, g);
 #pragma unroll
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
             }
         }
     };
-    if (post) load_post();
+    if (post && n > 0) load_post();  // (a group past the last row has no canvas)
     left = p.gate ? p.C - r0 % p.C : 0x7fffffff;
 #pragma unroll
     for (int k = 0; k < kNV; ++k) {

@@ -100,8 +100,8 @@ def test_norm_forward(B, C, d, T, P):
 
 
 # many rows: the form that keeps rows in flight, its widths full and not, canvases that end inside a
-# CTA's run of rows
-MANY = [(3, 500, 64), (256, 5, 72), (5, 300, 256), (4, 400, 512), (3, 401, 1000), (2, 700, 1024), (2, 700, 2048), (7, 200, 2056),
+# CTA's run of rows, last groups of a CTA with no row (3 x 500 of 64, 3 x 401 of 2048)
+MANY = [(3, 500, 64), (256, 5, 72), (5, 300, 256), (4, 400, 512), (3, 401, 1000), (2, 700, 1024), (2, 700, 2048), (3, 401, 2048), (7, 200, 2056),
         (2, 600, 4096), (3, 397, 5000), (1, 1200, 8192), (7, 171, 8200)]
 
 
