@@ -98,19 +98,26 @@ __device__ __forceinline__ void row_sums(float (&v)[kV], float* sh) {
     for (int i = 0; i < kV; ++i) v[i] = warp_sum(l < kWarps ? sh[i * kWarps + l] : 0.f);
 }
 
+// 1 / sqrt(x): the hardware's approximation and one Newton step (error about 2^-23).
+__device__ __forceinline__ float rsqrt_newton(float x) {
+    const float r = rsqrtf(x);
+    return r * fmaf(-0.5f * x * r, r, 1.5f);
+}
+
 // 1 / sqrt(mean f^2 + eps) of a row held in its threads' registers.  Squares leave fp32's range where values
 // are beyond about 1e19 or, with hardly any eps, below 1e-15; such a row (the choice is the same in all
 // its threads) is summed again in fp64.
 template <int kWarps, int kNV, int kN>
 __device__ __forceinline__ float row_rstd(const float (&f)[kNV][kN], float inv_d, float eps, float* sh, double* sh64) {
-    float s[1] = {0.f};
+    float a4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < kNV; ++k)
 #pragma unroll
-        for (int i = 0; i < kN; ++i) s[0] = fmaf(f[k][i], f[k][i], s[0]);
+        for (int i = 0; i < kN; ++i) a4[i & 3] = fmaf(f[k][i], f[k][i], a4[i & 3]);
+    float s[1] = {(a4[0] + a4[1]) + (a4[2] + a4[3])};
     row_sums<kWarps>(s, sh);
     const float ms = fmaf(s[0], inv_d, eps);
-    if (ms > 1e-30f && ms < INFINITY) return 1.0f / sqrtf(ms);
+    if (ms > 1e-30f && ms < INFINITY) return rsqrt_newton(ms);
     double a = 0.0;
 #pragma unroll
     for (int k = 0; k < kNV; ++k)
@@ -130,7 +137,8 @@ __device__ __forceinline__ float row_rstd(const float (&f)[kNV][kN], float inv_d
 
 // ------------------------------------------------------------------------------------ forward
 // One row per group of kWarps warps, kNV 16-byte vectors per thread, everything in registers: each
-// input is read once.  kWarps == 1: four rows per CTA, no barrier; else one row per CTA.
+// input is read once.  kWarps == 1: four rows per CTA, no barrier; else one row per CTA.  Every step is
+// rounded as in the ring below, so that a row's results do not depend on the number of rows.
 template <typename T, typename P, int kWarps, int kNV>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) block_norm_kernel(const __grid_constant__ BlockNormParams p) {
     constexpr int kN = Vec<T>::kN;
@@ -185,7 +193,7 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) block_norm_ke
                     for (int i = 0; i < kN; ++i) fw[i] *= fg[i];
                 }
 #pragma unroll
-                for (int i = 0; i < kN; ++i) fx[k][i] = fmaf(p.res_scale * (fy[k][i] * rstd), fw[i], fx[k][i]);
+                for (int i = 0; i < kN; ++i) fx[k][i] = fmaf(fy[k][i] * rstd, fw[i] * p.res_scale, fx[k][i]);
                 *reinterpret_cast<uint4*>(xo + c * kN) = Vec<T>::pack(fx[k]);
             }
         }
@@ -209,8 +217,8 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) block_norm_ke
 }
 
 // ------------------------------------------------------------------------------------ rows in a ring
-// With many rows a group of kW warps walks a run of them, the next rows' bulk copies in flight in a
-// ring of shared-memory slots with a barrier each.  Beside memory it is instructions that bound such a
+// A group of kW warps walks a run of rows, the next rows' bulk copies in flight in a ring of
+// shared-memory slots with a barrier each.  Beside memory it is instructions that bound such a
 // walk, so the parameters stay in registers, as fp32 pairs for the packed fma.rn.f32x2, and widths
 // that fill every thread's vectors (kFull) have no column checks.  A CTA has kGroups groups, each with
 // its own ring and named barrier.
@@ -234,12 +242,6 @@ __device__ __forceinline__ void load_pairs(const P* src, Pair (&p)[kP]) {
     load_params<2 * kP>(src, f);
 #pragma unroll
     for (int i = 0; i < kP; ++i) p[i] = pair(f[2 * i], f[2 * i + 1]);
-}
-
-// 1 / sqrt(x): the hardware's approximation and one Newton step (error about 2^-23).
-__device__ __forceinline__ float rsqrt_newton(float x) {
-    const float r = rsqrtf(x);
-    return r * fmaf(-0.5f * x * r, r, 1.5f);
 }
 
 constexpr int kMaxSlots = 8;
@@ -511,20 +513,19 @@ cudaError_t launch_forward(const BlockNormParams& p, cudaStream_t st) {
 template <typename T, typename P>
 cudaError_t forward_by_width(const BlockNormParams& p, cudaStream_t st) {
     const int n_vec = p.d / Vec<T>::kN;
-    if (p.R >= 8 * num_sms() && n_vec <= 1024) {
-        if (n_vec <= 32) return launch_rows<T, P, 1, 8, 1, 3>(p, st);
-        if (n_vec <= 64) return launch_rows<T, P, 1, 8, 2, 2>(p, st);
-        if (n_vec <= 128) return launch_rows<T, P, 2, 4, 2, 2>(p, st);
-        if (n_vec <= 256) return launch_rows<T, P, 4, 2, 2, 2>(p, st);
-        if (n_vec <= 512) return launch_rows<T, P, 8, 1, 2, 2>(p, st);
-        return launch_rows<T, P, 16, 1, 2, 1>(p, st);
-    }
-    if (n_vec <= 32) return launch_forward<T, P, 1, 1>(p, st);
-    if (n_vec <= 64) return launch_forward<T, P, 1, 2>(p, st);
-    if (n_vec <= 128) return launch_forward<T, P, 2, 2>(p, st);
-    if (n_vec <= 256) return launch_forward<T, P, 4, 2>(p, st);
-    if (n_vec <= 512) return launch_forward<T, P, 8, 2>(p, st);
-    if (n_vec <= 1024) return launch_forward<T, P, 16, 2>(p, st);
+    // Which form (us, bf16, both norms with a gate).  Up to 32 vectors a warp has a row, and the direct form's
+    // one load per thread is all there is to wait for (256 columns, 64, 4096 and 16384 rows: 2.3, 2.9, 7.0;
+    // the ring 2.6, 3.7, 8.3) until the rows are so many that memory is (65536 rows: 28.6, ring 22.6).  Wider,
+    // the ring, at any number of rows (2048 columns, 64, 4096 and 16384 rows: 2.7, 11.4, 43.6; direct 3.2,
+    // 14.9, 54.4), as long as the parameters of a thread's columns fit its registers and three rows the
+    // shared memory.
+    if (n_vec <= 32 && p.R < 256 * num_sms() && p.wait_limit <= 0) return launch_forward<T, P, 1, 1>(p, st);  // (no waits to test)
+    if (n_vec <= 32) return launch_rows<T, P, 1, 8, 1, 3>(p, st);
+    if (n_vec <= 64) return launch_rows<T, P, 1, 8, 2, 2>(p, st);
+    if (n_vec <= 128) return launch_rows<T, P, 2, 4, 2, 2>(p, st);
+    if (n_vec <= 256) return launch_rows<T, P, 4, 2, 2, 2>(p, st);
+    if (n_vec <= 512) return launch_rows<T, P, 8, 1, 2, 2>(p, st);
+    if (n_vec <= 1024) return launch_rows<T, P, 16, 1, 2, 1>(p, st);
     if (n_vec <= 2048) return launch_forward<T, P, 16, 4>(p, st);
     return launch_forward<T, P, 32, 4>(p, st);
 }

@@ -100,9 +100,10 @@ def test_norm_forward(B, C, d, T, P):
 
 
 # many rows: the form that keeps rows in flight, its widths full and not, canvases that end inside a
-# CTA's run of rows, last groups of a CTA with no row (3 x 500 of 64, 3 x 401 of 2048)
+# CTA's run of rows, groups of a CTA with no row (3 x 401 of 2048)
 MANY = [(3, 500, 64), (256, 5, 72), (5, 300, 256), (4, 400, 512), (3, 401, 1000), (2, 700, 1024), (2, 700, 2048), (3, 401, 2048), (7, 200, 2056),
-        (2, 600, 4096), (3, 397, 5000), (1, 1200, 8192), (7, 171, 8200)]
+        (2, 600, 4096), (3, 397, 5000), (1, 1200, 8192), (7, 171, 8200),
+        (3, 20001, 64), (200, 300, 72)]
 
 
 @pytest.mark.parametrize("T,P", [(BF16, BF16), (BF16, F32), (F32, F32)])
@@ -114,6 +115,17 @@ def test_norm_forward_many_rows(B, C, d, T, P):
         out = dg.dg_block_norm(x, w_pre, y=y, w_post=w_post, gate=gate, C=C, res_scale=0.7, eps=1e-6)
         check_forward(x, y, w_post, gate, w_pre, C, s, eps, out)
     assert dg.dg_device_error() == 0
+
+
+@pytest.mark.parametrize("T,d", [(BF16, 72), (BF16, 256), (F32, 128), (BF16, 2048), (F32, 2048)])
+def test_norm_row_results_do_not_depend_on_the_number_of_rows(T, d):
+    rows = 40000 if d <= 256 else 2000
+    x, y, w_post, gate, w_pre = norm_inputs(1, rows, d, T, F32, "both", True)
+    many = dg.dg_block_norm(x, w_pre, y=y, w_post=w_post, gate=gate, C=rows, res_scale=0.7)
+    for n in (1, 7, 900):
+        few = dg.dg_block_norm(x[:n], w_pre, y=y[:n], w_post=w_post, gate=gate, C=n, res_scale=0.7)
+        for key, value in few.items():
+            assert torch.equal(value, many[key][:n]), key
 
 
 @pytest.mark.parametrize("rows", [4, 500])
@@ -393,7 +405,7 @@ def check_block(z, w1, w1v, w2, w2v, got):
 
 
 @pytest.mark.parametrize("R,d,dff", [(1, 64, 64), (16, 64, 256), (5, 192, 320), (1, 1024, 4096), (130, 512, 2048), (256, 2048, 8192), (300, 128, 576), (2500, 320, 2112), (1100, 1024, 4096),
-                                     (32, 2048, 8192), (33, 2048, 8192), (31, 192, 64), (17, 4160, 128)])
+                                     (16, 2048, 8192), (32, 2048, 8192), (33, 2048, 8192), (31, 192, 64), (17, 4160, 128)])
 def test_block(R, d, dff):
     g = gen(R + d)
     z = randn(g, R, d, dtype=BF16)
