@@ -271,9 +271,10 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // GELU, tanh form, as x / (1 + exp(-2u)), two values at a time.  The hidden layer is rounded to 4 bits
 // by comparisons with the E2M1 midpoints, so an error here moves values across them: the hardware
 // tanh's 2^-11 would move one value in a few hundred, ex2 and a reciprocal (about 2^-22) one in a
-// million.  u is kept below 2^7, where the quotient is 2^-125 x and the reciprocal still a normal number.
-// (A reciprocal by Newton's iteration, off the special-function unit, was no faster: the epilogue's
-// 6000 cycles a tile are beside the products' 5700 already.)
+// million.  The special-function unit bounds the epilogue (without the gelu a block on 4096 rows of 1024 x
+// 4096 takes 27 us), so two values share a reciprocal: 1 / a = b (1 / ab); 31.8 us, with one each 32.6, with
+// Newton's iteration instead no less.  The exponent is kept below 62, so that ab and its reciprocal are
+// normal numbers: past it (x below about -7.5) the result is 2^-62 x instead of something smaller still.
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -284,9 +285,10 @@ __device__ __forceinline__ Pair gelu_pair(Pair x) {
     const float k1 = k0 * 0.044715f;
     float lo, hi;
     unpair(mul2(x, fma2(mul2(x, x), pair(k1, k1), pair(k0, k0))), lo, hi);
-    lo = rcp_approx(1.0f + ex2_approx(fminf(lo, 125.0f)));
-    hi = rcp_approx(1.0f + ex2_approx(fminf(hi, 125.0f)));
-    return mul2(x, pair(lo, hi));
+    lo = 1.0f + ex2_approx(fminf(lo, 62.0f));
+    hi = 1.0f + ex2_approx(fminf(hi, 62.0f));
+    const float r = rcp_approx(lo * hi);
+    return mul2(x, mul2(pair(r, r), pair(hi, lo)));
 }
 // max(a, |b|) that keeps a NaN.
 __device__ __forceinline__ float max_abs_nan(float a, float b) {
