@@ -182,9 +182,10 @@ enum Mx4OutKind : int {
     kMx4OutF32 = 1,
     kMx4OutGelu = 2,  // gelu of the product, quantised again
 };
-// Up to so many rows the product quantises a bf16 A itself: beyond, a launch of its own costs less than
-// every column tile's doing it again (a block of 1024 x 4096 x 1024 on 1, 16 and 32 rows: 11.6, 12.0 and 12.4 us,
-// with the launch 12.4, 12.8 and 12.5; of 2048 x 8192 x 2048: 16.2, 16.7 and 17.0, with the launch 16.8, 16.7 and 16.2).
+// Up to so many rows the product quantises a bf16 A itself (a block of 1024 x 4096 x 1024 on one row called from
+// Python, which takes longer than the GPU: 16.0 us, with a launch for the quantisation 19.3; captured, where the
+// launch costs little and the products start beside it: 11.7 and 10.7).  Beyond, every column tile's doing it
+// again costs more than the launch (2048 x 8192 x 2048 on 32 rows: 17.0 and 16.2).
 constexpr int32_t kMx4FewRows = 16;
 struct Mx4MatmulParams {
     const uint8_t *a, *a_scales, *w, *w_scales;

@@ -1050,19 +1050,27 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
 
 cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
     // Which kernel, from sizes alone (us a product, K = 2048 unless said):
-    //  * up to 128 rows half of a pair's tile would be empty: single CTAs, K split;
     //  * more 256 x 128 tiles than pairs: 256 x 256 tiles (96 tiles: 8.6, with 128 columns 10.2, single
     //    CTAs 14.7; a block on 4096 rows of 2048: 70, with 128 columns 83);
-    //  * fewer: 256 x 128 tiles (64 tiles: 7.0, single CTAs 8.2; 8 tiles: 6.5 and 6.9), unless splitting K
-    //    makes up for it, which takes K > 2048 (32 tiles at K = 8192: 14.9, split in two 12.5).
+    //  * fewer: 256 x 128 tiles (64 tiles: 7.0, single CTAs 8.2), unless splitting K makes up for it, which takes
+    //    K > 2048 (32 tiles at K = 8192: 14.9, split in two 12.5);
+    //  * up to 128 rows half of a pair's tile is empty, and single CTAs do better where they fit one wave
+    //    (128 tiles of 64 rows, K = 8192: 17.1, pairs 19.1; 256 tiles, K = 2048: 16.0, pairs 12.8) or four splits
+    //    shorten K > 1024 (16 tiles of 17 rows: 5.3, pairs 6.1; 32 tiles of 64 rows, K = 1024: 6.0, pairs 5.2; 64
+    //    tiles of 64 rows, two splits: 7.2, pairs 6.7);
+    //  * up to 16 rows single CTAs: their epilogue is as short as the pairs' (8 tiles of a row: 4.7, pairs 4.8).
     const int64_t pairs = static_cast<int64_t>((q.M + 255) / 256) * ((q.N + 127) / 128);
     const int64_t singles = static_cast<int64_t>((q.M + kMTile - 1) / kMTile) * ((q.N + kNTile - 1) / kNTile);
     const int32_t k_blocks = (q.K + kKStage - 1) / kKStage;
     // single CTAs: split K while the clusters fit one wave and every split keeps a block.  (Clusters of
-    // eight are placed two to a GPC at most: 200 x 1000 x 4096 took 10.8 us split in eight, 7.5 in four.)
+    // eight are placed two to a GPC at most: 200 x 1000 x 4096 took 10.8 us split in eight, 7.5 in four.  GPCs
+    // hold unequal numbers of SMs, so not all 148 take clusters of four: 33 tiles in four splits, K = 6624, 100
+    // rows, 9.8 us, 34 tiles 16.1, and 38 in two 11.3.  Every GPC of 16 SMs or more has room for four.)
     int splits = 1;
-    while (splits < 4 && 2 * splits * singles <= num_sms() && 2 * splits <= k_blocks) splits *= 2;
-    if (q.M > 128 && (splits == 1 || k_blocks <= 8)) {
+    while (splits < 4 && 2 * splits * singles <= (splits == 1 ? num_sms() : 128) && 2 * splits <= k_blocks) splits *= 2;
+    const bool paired = q.M > 128 ? splits == 1 || k_blocks <= 8
+                                  : q.M > 16 && (k_blocks <= 4 || (k_blocks <= 8 && splits == 2) || singles > num_sms());
+    if (paired) {
         const bool wide = 2 * pairs > num_sms();
         if (q.out_kind == kMx4OutF32) return wide ? launch_pair<kOutF32, 256>(q, st) : launch_pair<kOutF32, 128>(q, st);
         if (q.out_kind == kMx4OutBf16) return wide ? launch_pair<kOutBf16, 256>(q, st) : launch_pair<kOutBf16, 128>(q, st);
