@@ -523,8 +523,8 @@ cudaError_t forward_by_width(const BlockNormParams& p, cudaStream_t st) {
     // the ring 2.6, 3.7, 8.3) until the rows are so many that memory is (65536 rows: 28.6, ring 22.6).  Wider,
     // the ring, at any number of rows (2048 columns, 64, 4096 and 16384 rows: 2.7, 11.4, 43.6; direct 3.2,
     // 14.9, 54.4), as long as the parameters of a thread's columns fit its registers and three rows the
-    // shared memory.
-    if (n_vec <= 32 && p.R < 256 * num_sms() && p.wait_limit <= 0) return launch_forward<T, P, 1, 1>(p, st);  // (no waits to test)
+    // shared memory.  (The test hook's bounded waits are the ring's.)
+    if (n_vec <= 32 && p.R < 256 * num_sms() && p.wait_limit <= 0) return launch_forward<T, P, 1, 1>(p, st);
     if (n_vec <= 32) return launch_rows<T, P, 1, 8, 1, 3>(p, st);
     if (n_vec <= 64) return launch_rows<T, P, 1, 8, 2, 2>(p, st);
     if (n_vec <= 128) return launch_rows<T, P, 2, 4, 2, 2>(p, st);
@@ -552,6 +552,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) block_norm_backward_kernel(con
     constexpr int kN = Vec<T>::kN;
     constexpr int kThreads = 32 * kWarps;
     __shared__ float sh[2][3 * kWarps];
+    grid_launch_dependents();  // (the sums' kernel waits for this one's end)
     const int t = threadIdx.x;
     const int n_vec = p.d / kN;
     const int b = blockIdx.x / p.runs, run = blockIdx.x - b * p.runs;
@@ -636,7 +637,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) block_norm_backward_kernel(con
             }
         }
     }
-    grid_launch_dependents();
     // partial sums of the run: [B * runs, d] for each of the two (the absent one is not stored)
 #pragma unroll
     for (int k = 0; k < kNV; ++k) {
@@ -658,16 +658,21 @@ __global__ void __launch_bounds__(32 * kWarps, 1) block_norm_backward_kernel(con
 
 // The same with the rows' bulk copies kept in flight (see block_norm_rows_kernel).  A CTA's rows are of
 // one canvas; its groups take them in turn, and their columns' sums are added at the end, in the
-// order of the groups.  12288 x 2048 bf16, gated: 60 us, and 65 with the sums below (4.6 TB/s);
+// order of the groups.  12288 x 2048 bf16, gated: 62.7 us with the sums below (4.8 TB/s);
 // an instruction is issued in 58 % of the cycles, so arithmetic and the exchange of a row's sums bound it as
-// much as memory (53 % busy).  1024 x 4096 fp32: 26 us, read twice as above 31.
+// much as memory (53 % busy).  1024 x 4096 fp32: 26 us, read twice as above 31.  Rows of up to 32 vectors are
+// too small for bulk copies (four of 128 bytes a row: 16384 x 64 bf16 took 19.3 us) and come by loads three rows
+// ahead (15.5 us).
 template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas, bool kFull>
 __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
     block_norm_backward_rows_kernel(const __grid_constant__ BlockNormBackwardParams p, int slots) {
     constexpr int kN = Vec<T>::kN, kP = kN / 2, kThreads = 32 * kW;
+    constexpr bool kRing = kNV > 1;  // one vector per thread: rows come straight into registers
+    constexpr int kAhead = 3;        // so many of them
     extern __shared__ __align__(128) uint8_t slots_mem[];
     __shared__ Rings<kGroups> rings;
     __shared__ __align__(16) float sh[kGroups][2][3 * kW];
+    grid_launch_dependents();  // (the sums' kernel waits for this one's end)
     const int group = threadIdx.x / kThreads, t = threadIdx.x % kThreads;
     const int n_vec = kFull ? kNV * kThreads : p.d / kN, d = kFull ? kNV * kThreads * kN : p.d;
     const int b = blockIdx.x / p.runs, part = blockIdx.x - b * p.runs;
@@ -680,7 +685,7 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
     const uint32_t at_h = up ? row_bytes : 0, at_x = at_h + (pre ? row_bytes : 0), at_y = at_x + (pre ? row_bytes : 0);
     const uint32_t slot_bytes = at_y + (post ? row_bytes : 0);
     uint8_t* ring = slots_mem + group * slots * slot_bytes;
-    rings_init(rings, p.wait_limit);
+    if (kRing) rings_init(rings, p.wait_limit);
     const int ahead = min(n, slots);  // rows fetched before the walk; slot s is always filled by thread s
     int64_t next = r0 + (t < ahead ? t : 0) * kGroups;
     int fills = 0;
@@ -698,7 +703,21 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
         next += slots * kGroups;
         ++fills;
     };
-    if (t < ahead) fetch(t);
+    if (kRing && t < ahead) fetch(t);
+    uint4 row[kAhead][4];
+    const auto load_row = [&](int i, uint4(&v)[4]) {
+        const int64_t r = r0 + static_cast<int64_t>(i) * kGroups;
+        const bool in = i < n && t < n_vec;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        v[0] = in && up ? load16(static_cast<const T*>(p.dx_out) + r * p.ld_dx_out + t * kN) : zero;
+        v[1] = in && pre ? load16(static_cast<const T*>(p.dh) + r * p.ld_dh + t * kN) : zero;
+        v[2] = in && pre ? load16(static_cast<const T*>(p.x) + r * p.ld_x + t * kN) : zero;
+        v[3] = in && post ? load16(static_cast<const T*>(p.y) + r * p.ld_y + t * kN) : zero;
+    };
+    if (!kRing) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load_row(i, row[i]);
+    }
     Pair wp[kNV][kP], wc[kNV][kP], acc_pre[kNV][kP], acc_post[kNV][kP];
     const Pair scale = pair(p.res_scale, p.res_scale);
 #pragma unroll
@@ -736,10 +755,17 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
         const float rx_next = pre && more ? *rstd_x : 0.f, ry_next = post && more ? *rstd_y : 0.f;
         const Pair rx2 = pair(rx, rx), ry2 = pair(ry, ry);
         DG_CHECK(g_device_error, (r0 + i * kGroups) / p.C == b && b < p.B);
-        mbar_wait(&rings.full[group][slot], phase, &rings.wc);
+        if (kRing) mbar_wait(&rings.full[group][slot], phase, &rings.wc);
         const uint8_t* src = src0 + slot * slot_bytes;
         // a vector's columns of the four rows (zero where the call has none)
         const auto read = [&](int k, Pair(&g)[kP], Pair(&h)[kP], Pair(&x)[kP], Pair(&y)[kP]) {
+            if (!kRing) {
+                unpack_pairs<T>(row[0][0], g);
+                unpack_pairs<T>(row[0][1], h);
+                unpack_pairs<T>(row[0][2], x);
+                unpack_pairs<T>(row[0][3], y);
+                return;
+            }
             const bool in = kFull || t + k * kThreads < n_vec;
             const uint8_t* at = src + k * (16 * kThreads);
             const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -766,7 +792,7 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
         if (kW == 1) group_barrier<kW>(group);
         // past this barrier every thread is done with the row before: its slot is free
         const int before = slot == 0 ? slots - 1 : slot - 1;
-        if (t == before && i > 0 && i - 1 + slots < n) fetch(before);
+        if (kRing && t == before && i > 0 && i - 1 + slots < n) fetch(before);
         const float a = -rx * s[0] * inv_d, e = -ry * fmaf(a, s[2], s[1]) * inv_d;
         const Pair a2 = pair(a, a), e2 = pair(e, e);
 #pragma unroll
@@ -789,13 +815,20 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
         }
         rx = rx_next;
         ry = ry_next;
+        if (!kRing) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int q = 1; q < kAhead; ++q) row[q - 1][j] = row[q][j];
+            }
+            load_row(i + kAhead, row[kAhead - 1]);
+        }
         if (++slot == slots) {
             slot = 0;
             phase ^= 1;
         }
     }
-    rings_drain(rings, group, t, fills);
-    grid_launch_dependents();
+    if (kRing) rings_drain(rings, group, t, fills);
     // the groups' sums, by way of the ring's memory: group 0 adds the others' to its own
     for (int which = 0; which < 2; ++which) {
         if (which == 0 ? !pre : !post) continue;
@@ -848,8 +881,9 @@ __device__ __forceinline__ float4 param4(const __nv_bfloat16* p) {
 
 // Adds the runs' partial sums, blockIdx.y 0: dw_pre, 1: dw_post and dgate.  A CTA takes 32 columns:
 // eight threads of four columns (a 128-byte line of a run's sums) by 32 lanes that share the runs.  Of
-// the lanes, `sub` (a power of two) share a canvas; every sum has a fixed order.  Bound by the trips to L2
-// of a lane's run of loads: about 5 us behind the kernel above for 2 x 296 rows of 2048 sums (4.8 MB).
+// the lanes, `sub` (a power of two) share a canvas, or with more than 16 canvases each has every 32nd, four at
+// a time; every sum has a fixed order.  Bound by the trips to L2 of a lane's run of loads: 3 to 5 us behind the
+// kernel above for 2 x 296 rows of 2048 sums (4.8 MB).
 template <typename P>
 __global__ void __launch_bounds__(256) block_norm_params_kernel(const __grid_constant__ BlockNormBackwardParams p, int sub) {
     __shared__ float4 sh[32][8];
@@ -860,34 +894,54 @@ __global__ void __launch_bounds__(256) block_norm_params_kernel(const __grid_con
     if (!post) sub = 32;
     const int canvases = post ? p.B : 1, runs = post ? p.runs : p.B * p.runs;
     const int first = ty / sub, l = ty % sub;
-    float4 total = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool gated = post && p.gate;
+    const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 w = gated && in ? param4(static_cast<const P*>(p.w_post) + c) : one;
+    float4 total = zero;
     grid_dependency_wait();
-    for (int b0 = 0; b0 < canvases; b0 += 32 / sub) {  // one turn unless sub == 1
-        const int b = b0 + first;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (in && b < canvases) {
-            const float* src = part + static_cast<int64_t>(b) * runs * p.d + c;
-#pragma unroll 8
-            for (int j = l; j < runs; j += sub) a = add4(a, __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(j) * p.d)));
+    constexpr int kTurns = 4;  // canvases of a lane whose loads are in flight together
+    for (int b0 = 0; b0 < canvases; b0 += kTurns * 32 / sub) {  // one turn, and its first canvas only, unless sub == 1
+        float4 a[kTurns], g[kTurns];
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k) {
+            const int b = b0 + first + k * 32;
+            a[k] = zero;
+            g[k] = gated && in && b < canvases ? param4(static_cast<const P*>(p.gate) + static_cast<int64_t>(b) * p.d + c) : one;
         }
+        const auto add_run = [&](int k, int j) {
+            const int b = b0 + first + k * 32;
+            if (in && b < canvases) a[k] = add4(a[k], __ldcg(reinterpret_cast<const float4*>(part + (static_cast<int64_t>(b) * runs + j) * p.d + c)));
+        };
         if (sub > 1) {
-            sh[ty][tx] = a;
-            __syncthreads();
-            if (l == 0)
-                for (int q = 1; q < sub; ++q) a = add4(a, sh[ty + q][tx]);
-            __syncthreads();
-        }
-        if (l != 0 || !in || b >= canvases) continue;
-        if (post) {
-            a = make_float4(p.res_scale * a.x, p.res_scale * a.y, p.res_scale * a.z, p.res_scale * a.w);
-            if (p.gate) {
-                const int64_t at = static_cast<int64_t>(b) * p.d + c;
-                const float4 g = param4(static_cast<const P*>(p.gate) + at), w = param4(static_cast<const P*>(p.w_post) + c);
-                *reinterpret_cast<float4*>(p.dgate + at) = make_float4(w.x * a.x, w.y * a.y, w.z * a.z, w.w * a.w);
-                a = make_float4(g.x * a.x, g.y * a.y, g.z * a.z, g.w * a.w);
+#pragma unroll 8
+            for (int j = l; j < runs; j += sub) add_run(0, j);
+        } else {
+#pragma unroll 2
+            for (int j = 0; j < runs; ++j) {
+#pragma unroll
+                for (int k = 0; k < kTurns; ++k) add_run(k, j);
             }
         }
-        total = add4(total, a);
+        if (sub > 1) {
+            sh[ty][tx] = a[0];
+            __syncthreads();
+            if (l == 0)
+                for (int q = 1; q < sub; ++q) a[0] = add4(a[0], sh[ty + q][tx]);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k) {
+            const int b = b0 + first + k * 32;
+            if (l != 0 || !in || b >= canvases) continue;
+            if (post) {
+                a[k] = make_float4(p.res_scale * a[k].x, p.res_scale * a[k].y, p.res_scale * a[k].z, p.res_scale * a[k].w);
+                if (gated)
+                    *reinterpret_cast<float4*>(p.dgate + static_cast<int64_t>(b) * p.d + c) =
+                        make_float4(w.x * a[k].x, w.y * a[k].y, w.z * a[k].z, w.w * a[k].w);
+                a[k] = make_float4(g[k].x * a[k].x, g[k].y * a[k].y, g[k].z * a[k].z, g[k].w * a[k].w);
+            }
+            total = add4(total, a[k]);
+        }
     }
     sh[ty][tx] = total;
     __syncthreads();
@@ -930,7 +984,7 @@ cudaError_t launch_backward_rows_as(const BlockNormBackwardParams& p, cudaStream
     constexpr int kRingBytes = 200 * 1024 / kCtas;
     const int slot = p.d * static_cast<int>(sizeof(T)) * ((p.dx_out ? 1 : 0) + (p.w_pre ? 2 : 0) + (p.y ? 1 : 0));
     const int slots = std::min(kMaxSlots, kRingBytes / (slot * kGroups));
-    const int bytes = std::max(kGroups * slots * slot, (kGroups - 1) * p.d * 4);
+    const int bytes = std::max(kNV > 1 ? kGroups * slots * slot : 0, (kGroups - 1) * p.d * 4);
     static DeviceOnce once;
     const cudaError_t attr_err = allow_shared_memory(once, block_norm_backward_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull>, kRingBytes);
     if (attr_err != cudaSuccess) return attr_err;
