@@ -490,9 +490,9 @@ template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas, bool 
 cudaError_t launch_rows_as(const BlockNormParams& p, cudaStream_t st) {
     constexpr int kRingBytes = 200 * 1024 / kCtas;
     const int slot = p.d * static_cast<int>(sizeof(T)) * (p.y ? 2 : 1);
-    const int slots = std::min(kMaxSlots, kRingBytes / (slot * kGroups));
     const int64_t groups = static_cast<int64_t>(kCtas) * num_sms() * kGroups;
     const int run = static_cast<int>((p.R + groups - 1) / groups);
+    const int slots = std::min({kMaxSlots, run, kRingBytes / (slot * kGroups)});
     const int64_t ctas = (p.R + static_cast<int64_t>(run) * kGroups - 1) / (static_cast<int64_t>(run) * kGroups);
     static DeviceOnce once;
     const cudaError_t attr_err = allow_shared_memory(once, block_norm_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull>, kRingBytes);
@@ -983,7 +983,7 @@ template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas, bool 
 cudaError_t launch_backward_rows_as(const BlockNormBackwardParams& p, cudaStream_t st) {
     constexpr int kRingBytes = 200 * 1024 / kCtas;
     const int slot = p.d * static_cast<int>(sizeof(T)) * ((p.dx_out ? 1 : 0) + (p.w_pre ? 2 : 0) + (p.y ? 1 : 0));
-    const int slots = std::min(kMaxSlots, kRingBytes / (slot * kGroups));
+    const int slots = std::min({kMaxSlots, (p.run_rows + kGroups - 1) / kGroups, kRingBytes / (slot * kGroups)});
     const int bytes = std::max(kNV > 1 ? kGroups * slots * slot : 0, (kGroups - 1) * p.d * 4);
     static DeviceOnce once;
     const cudaError_t attr_err = allow_shared_memory(once, block_norm_backward_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull>, kRingBytes);
