@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) block_norm_backward_kernel(con
 // one canvas; its groups take them in turn, and their columns' sums are added at the end, in the
 // order of the groups.  12288 x 2048 bf16, gated: 62.7 us with the sums below (4.8 TB/s);
 // an instruction is issued in 58 % of the cycles, so arithmetic and the exchange of a row's sums bound it as
-// much as memory (53 % busy).  1024 x 4096 fp32: 26 us, read twice as above 31.  Rows of up to 32 vectors are
+// much as memory (54 % busy).  1024 x 4096 fp32: 26 us, read twice as above 31.  Rows of up to 32 vectors are
 // too small for bulk copies (four of 128 bytes a row: 16384 x 64 bf16 took 19.3 us) and come by loads three rows
 // ahead (15.5 us).
 template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas, bool kFull>
@@ -882,7 +882,7 @@ __device__ __forceinline__ float4 param4(const __nv_bfloat16* p) {
 // Adds the runs' partial sums, blockIdx.y 0: dw_pre, 1: dw_post and dgate.  A CTA takes 32 columns:
 // eight threads of four columns (a 128-byte line of a run's sums) by 32 lanes that share the runs.  Of
 // the lanes, `sub` (a power of two) share a canvas, or with more than 16 canvases each has every 32nd, four at
-// a time; every sum has a fixed order.  Bound by the trips to L2 of a lane's run of loads: 3 to 5 us behind the
+// a time; every sum has a fixed order.  Bound by the trips to L2 of a lane's run of loads: 2 to 3 us behind the
 // kernel above for 2 x 296 rows of 2048 sums (4.8 MB).
 template <typename P>
 __global__ void __launch_bounds__(256) block_norm_params_kernel(const __grid_constant__ BlockNormBackwardParams p, int sub) {

@@ -331,7 +331,9 @@ def check_product(a, av, w, wv, dtype, **kw):
                                    # many tiles: ragged rows and columns, one row in the last pair of row tiles, K ending in
                                    # every part of a stage, more tiles than pairs of CTAs
                                    (2048, 2056, 480), (257, 9608, 96), (4000, 1288, 1184), (2000, 4096, 2048), (2305, 2312, 320),
-                                   (5000, 3000, 64), (4096, 2048, 800)])
+                                   (5000, 3000, 64), (4096, 2048, 800),
+                                   # up to 128 rows: pairs, single CTAs with and without a split, more columns than one wave
+                                   (17, 136, 1056), (128, 264, 2112), (100, 4608, 1312), (100, 9736, 2208), (20, 19080, 160)])
 def test_product(M, N, K):
     g = gen(M + N + K)
     (a, av), (w, wv) = random_mx4(g, M, K), random_mx4(g, N, K)
@@ -405,7 +407,7 @@ def check_block(z, w1, w1v, w2, w2v, got):
 
 
 @pytest.mark.parametrize("R,d,dff", [(1, 64, 64), (16, 64, 256), (5, 192, 320), (1, 1024, 4096), (130, 512, 2048), (256, 2048, 8192), (300, 128, 576), (2500, 320, 2112), (1100, 1024, 4096),
-                                     (16, 2048, 8192), (32, 2048, 8192), (33, 2048, 8192), (31, 192, 64), (17, 4160, 128)])
+                                     (16, 2048, 8192), (32, 2048, 8192), (33, 2048, 8192), (31, 192, 64), (17, 4160, 128), (100, 2112, 2048), (128, 64, 128)])
 def test_block(R, d, dff):
     g = gen(R + d)
     z = randn(g, R, d, dtype=BF16)
