@@ -656,19 +656,29 @@ __global__ void __launch_bounds__(32 * kWarps, 1) block_norm_backward_kernel(con
     }
 }
 
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+__device__ __forceinline__ void store_pairs(float* to, Pair a, Pair b) {
+    float4 v;
+    unpair(a, v.x, v.y);
+    unpair(b, v.z, v.w);
+    *reinterpret_cast<float4*>(to) = v;
+}
+
 // The same with the rows' bulk copies kept in flight (see block_norm_rows_kernel).  A CTA's rows are of
 // one canvas; its groups take them in turn, and their columns' sums are added at the end, in the
-// order of the groups.  12288 x 2048 bf16, gated: 62.7 us with the sums below (4.8 TB/s);
+// order of the groups.  12288 x 2048 bf16, gated: 61.9 us with the sums below (4.9 TB/s);
 // an instruction is issued in 58 % of the cycles, so arithmetic and the exchange of a row's sums bound it as
 // much as memory (54 % busy).  1024 x 4096 fp32: 26 us, read twice as above 31.  Rows of up to 32 vectors are
-// too small for bulk copies (four of 128 bytes a row: 16384 x 64 bf16 took 19.3 us) and come by loads three rows
-// ahead (15.5 us).
+// too small for bulk copies (four of 128 bytes a row: 16384 x 64 bf16 took 19.3 us) and come by loads two rows ahead
+// (14.0 us; three spill).
 template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas, bool kFull>
 __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
     block_norm_backward_rows_kernel(const __grid_constant__ BlockNormBackwardParams p, int slots) {
     constexpr int kN = Vec<T>::kN, kP = kN / 2, kThreads = 32 * kW;
     constexpr bool kRing = kNV > 1;  // one vector per thread: rows come straight into registers
-    constexpr int kAhead = 3;        // so many of them
+    constexpr int kAhead = 2;        // so many of them
     extern __shared__ __align__(128) uint8_t slots_mem[];
     __shared__ Rings<kGroups> rings;
     __shared__ __align__(16) float sh[kGroups][2][3 * kW];
@@ -829,49 +839,38 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
         }
     }
     if (kRing) rings_drain(rings, group, t, fills);
-    // the groups' sums, by way of the ring's memory: group 0 adds the others' to its own
-    for (int which = 0; which < 2; ++which) {
-        if (which == 0 ? !pre : !post) continue;
-        float* sums = reinterpret_cast<float*>(slots_mem);  // [kGroups - 1, d]
-        if (group > 0) {
+    // the columns' sums: of one group as they are, of more by way of the ring's memory, [2, kGroups, d]
+    const int64_t out = static_cast<int64_t>(blockIdx.x) * p.d;
+    float* sums = reinterpret_cast<float*>(slots_mem);
+    float* to_pre = kGroups == 1 ? p.part_pre + out : sums + group * p.d;
+    float* to_post = kGroups == 1 ? p.part_post + out : sums + (kGroups + group) * p.d;
 #pragma unroll
-            for (int k = 0; k < kNV; ++k) {
-                const int c = t + k * kThreads;
-                if (c < n_vec) {
+    for (int k = 0; k < kNV; ++k) {
+        const int c = t + k * kThreads;
+        if (kFull || c < n_vec) {
 #pragma unroll
-                    for (int i = 0; i < kP; ++i)
-                        *reinterpret_cast<Pair*>(sums + (group - 1) * p.d + c * kN + 2 * i) = which == 0 ? acc_pre[k][i] : acc_post[k][i];
-                }
+            for (int i = 0; i < kP; i += 2) {
+                if (pre) store_pairs(to_pre + c * kN + 2 * i, acc_pre[k][i], acc_pre[k][i + 1]);
+                if (post) store_pairs(to_post + c * kN + 2 * i, acc_post[k][i], acc_post[k][i + 1]);
             }
         }
+    }
+    if (kGroups > 1) {
         __syncthreads();
-        if (group == 0) {
-            float* out = (which == 0 ? p.part_pre : p.part_post) + static_cast<int64_t>(blockIdx.x) * p.d;
+#pragma unroll 1
+        for (int c = 4 * threadIdx.x; c < p.d; c += 4 * kThreads * kGroups) {
+            for (int which = 0; which < 2; ++which) {
+                if (which == 0 ? !pre : !post) continue;
+                const float* src = sums + which * kGroups * p.d + c;
+                float4 v = *reinterpret_cast<const float4*>(src);
 #pragma unroll
-            for (int k = 0; k < kNV; ++k) {
-                const int c = t + k * kThreads;
-                if (c < n_vec) {
-#pragma unroll
-                    for (int i = 0; i < kP; ++i) {
-                        float lo, hi;
-                        unpair(which == 0 ? acc_pre[k][i] : acc_post[k][i], lo, hi);
-                        for (int q = 0; q < kGroups - 1; ++q) {
-                            const float2 o = *reinterpret_cast<const float2*>(sums + q * p.d + c * kN + 2 * i);
-                            lo += o.x;
-                            hi += o.y;
-                        }
-                        *reinterpret_cast<float2*>(out + c * kN + 2 * i) = make_float2(lo, hi);
-                    }
-                }
+                for (int q = 1; q < kGroups; ++q) v = add4(v, *reinterpret_cast<const float4*>(src + q * p.d));
+                *reinterpret_cast<float4*>((which == 0 ? p.part_pre : p.part_post) + out + c) = v;
             }
         }
-        __syncthreads();
     }
 }
 
-__device__ __forceinline__ float4 add4(float4 a, float4 b) {
-    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-}
 __device__ __forceinline__ float4 param4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ float4 param4(const __nv_bfloat16* p) {
     float f[4];
@@ -984,7 +983,7 @@ cudaError_t launch_backward_rows_as(const BlockNormBackwardParams& p, cudaStream
     constexpr int kRingBytes = 200 * 1024 / kCtas;
     const int slot = p.d * static_cast<int>(sizeof(T)) * ((p.dx_out ? 1 : 0) + (p.w_pre ? 2 : 0) + (p.y ? 1 : 0));
     const int slots = std::min({kMaxSlots, (p.run_rows + kGroups - 1) / kGroups, kRingBytes / (slot * kGroups)});
-    const int bytes = std::max(kNV > 1 ? kGroups * slots * slot : 0, (kGroups - 1) * p.d * 4);
+    const int bytes = std::max(kNV > 1 ? kGroups * slots * slot : 0, kGroups > 1 ? 2 * kGroups * p.d * 4 : 0);
     static DeviceOnce once;
     const cudaError_t attr_err = allow_shared_memory(once, block_norm_backward_rows_kernel<T, P, kW, kGroups, kNV, kCtas, kFull>, kRingBytes);
     if (attr_err != cudaSuccess) return attr_err;
