@@ -883,7 +883,7 @@ __device__ __forceinline__ float4 param4(const __nv_bfloat16* p) {
 // the lanes, `sub` (a power of two) share a canvas, or with more than 16 canvases each has every 32nd, four at
 // a time; every sum has a fixed order.  Bound by the trips to L2 of a lane's run of loads: 2 to 3 us behind the
 // kernel above for 2 x 296 rows of 2048 sums (4.8 MB).
-template <typename P>
+template <typename P, int kTurns>
 __global__ void __launch_bounds__(256) block_norm_params_kernel(const __grid_constant__ BlockNormBackwardParams p, int sub) {
     __shared__ float4 sh[32][8];
     const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
@@ -898,8 +898,7 @@ __global__ void __launch_bounds__(256) block_norm_params_kernel(const __grid_con
     const float4 w = gated && in ? param4(static_cast<const P*>(p.w_post) + c) : one;
     float4 total = zero;
     grid_dependency_wait();
-    constexpr int kTurns = 4;  // canvases of a lane whose loads are in flight together
-    for (int b0 = 0; b0 < canvases; b0 += kTurns * 32 / sub) {  // one turn, and its first canvas only, unless sub == 1
+    for (int b0 = 0; b0 < canvases; b0 += kTurns * 32) {  // one turn, and its first canvas only, unless sub == 1
         float4 a[kTurns], g[kTurns];
 #pragma unroll
         for (int k = 0; k < kTurns; ++k) {
@@ -911,7 +910,7 @@ __global__ void __launch_bounds__(256) block_norm_params_kernel(const __grid_con
             const int b = b0 + first + k * 32;
             if (in && b < canvases) a[k] = add4(a[k], __ldcg(reinterpret_cast<const float4*>(part + (static_cast<int64_t>(b) * runs + j) * p.d + c)));
         };
-        if (sub > 1) {
+        if (kTurns == 1 || sub > 1) {
 #pragma unroll 8
             for (int j = l; j < runs; j += sub) add_run(0, j);
         } else {
@@ -966,7 +965,11 @@ cudaError_t launch_params(const BlockNormBackwardParams& p, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, block_norm_params_kernel<P>, p, sub);
+    // With one canvas to a lane and more CTAs than the SMs hold at 96 registers, the form of 40 (1024 x 8192 fp32 in
+    // four canvases: 60.5 us, else 63.7; with fewer CTAs it is the slower one, 4096 x 1024 in 16: 22.2 and 19.6).
+    e = sub > 1 && static_cast<int>(cfg.gridDim.x * cfg.gridDim.y) > 2 * num_sms()
+            ? cudaLaunchKernelEx(&cfg, block_norm_params_kernel<P, 1>, p, sub)
+            : cudaLaunchKernelEx(&cfg, block_norm_params_kernel<P, 4>, p, sub);
     if (e != cudaSuccess) return e;
     note_launches(1);
     return cudaGetLastError();
