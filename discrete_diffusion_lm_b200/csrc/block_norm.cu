@@ -250,7 +250,7 @@ __device__ __forceinline__ void load_pairs(const P* src, Pair (&p)[kP]) {
 }
 
 constexpr int kMaxSlots = 8;
-constexpr int kNormCtas = 2;  // per SM, of the backward pass: its parameters and sums take 125 registers
+constexpr int kNormCtas = 2;  // per SM, of the backward pass: its parameters and sums take 124 registers
 template <int kGroups>
 struct Rings {
     uint64_t full[kGroups][kMaxSlots];
@@ -669,8 +669,8 @@ __device__ __forceinline__ void store_pairs(float* to, Pair a, Pair b) {
 // The same with the rows' bulk copies kept in flight (see block_norm_rows_kernel).  A CTA's rows are of
 // one canvas; its groups take them in turn, and their columns' sums are added at the end, in the
 // order of the groups.  12288 x 2048 bf16, gated: 61.9 us with the sums below (4.9 TB/s);
-// an instruction is issued in 58 % of the cycles, so arithmetic and the exchange of a row's sums bound it as
-// much as memory (54 % busy).  1024 x 4096 fp32: 26 us, read twice as above 31.  Rows of up to 32 vectors are
+// an instruction is issued in 59 % of the cycles, so arithmetic and the exchange of a row's sums bound it as
+// much as memory (55 % busy).  1024 x 4096 fp32: 26 us, read twice as above 31.  Rows of up to 32 vectors are
 // too small for bulk copies (four of 128 bytes a row: 16384 x 64 bf16 took 19.3 us) and come by loads two rows ahead
 // (14.0 us; three spill).
 template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas, bool kFull>
