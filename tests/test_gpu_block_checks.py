@@ -16,6 +16,6 @@ def test_block_operators_under_the_checks_library():
     build.build(checks=True)
     env = dict(os.environ, DG_LIB="checks")
     r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_gpu_block_ops.py", "-x", "-q", "-m", "gpu", "-k",
-                        "many_rows or norm_backward or quantize or product or test_block or path"],
+                        "norm_forward or norm_row or norm_backward or quantize or product or test_block or path"],
                        cwd=ROOT, env=env, capture_output=True, text=True, timeout=900)
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-1000:]
