@@ -268,27 +268,28 @@ __device__ __forceinline__ uint32_t cluster_size() {
     return r;
 }
 
-// GELU, tanh form, as x / (1 + exp(-2u)), two values at a time.  The hidden layer is rounded to 4 bits
-// by comparisons with the E2M1 midpoints, so an error here moves values across them: the hardware
+// GELU, tanh form, as x T / (1 + T) with T = exp(2u), two values at a time.  The hidden layer is rounded to 4
+// bits by comparisons with the E2M1 midpoints, so an error here moves values across them: the hardware
 // tanh's 2^-11 would move one value in a few hundred, ex2 and a reciprocal (about 2^-22) one in a
 // million.  The special-function unit bounds the epilogue (without the gelu a block on 4096 rows of 1024 x
 // 4096 takes 27 us), so two values share a reciprocal: 1 / a = b (1 / ab); 31.8 us, with one each 32.6, with
-// Newton's iteration instead no less.  The exponent is kept below 62, so that ab and its reciprocal are
-// normal numbers: past it (x below about -7.5) the result is 2^-62 x instead of something smaller still.
+// Newton's iteration instead no less.  T is kept below 2^62, so that ab and its reciprocal are normal numbers (from
+// 2^24 on T / (1 + T) is 1 anyway); below, T goes to zero as it should, at 2^-126.  A sum that left fp32 gives no
+// number on either side; taking -infinity for 0, two instructions more for each pair, cost 1.7 us.
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ Pair gelu_pair(Pair x) {
-    const float k0 = -2.0f * 0.7978845608028654f * kLog2e;  // -2 sqrt(2 / pi) log2 e
+    const float k0 = 2.0f * 0.7978845608028654f * kLog2e;  // 2 sqrt(2 / pi) log2 e
     const float k1 = k0 * 0.044715f;
     float lo, hi;
     unpair(mul2(x, fma2(mul2(x, x), pair(k1, k1), pair(k0, k0))), lo, hi);
-    lo = 1.0f + ex2_approx(fminf(lo, 62.0f));
-    hi = 1.0f + ex2_approx(fminf(hi, 62.0f));
-    const float r = rcp_approx(lo * hi);
-    return mul2(x, mul2(pair(r, r), pair(hi, lo)));
+    lo = ex2_approx(fminf(lo, 62.0f));
+    hi = ex2_approx(fminf(hi, 62.0f));
+    const float a = 1.0f + lo, b = 1.0f + hi, r = rcp_approx(a * b);
+    return mul2(x, mul2(pair(lo, hi), mul2(pair(r, r), pair(b, a))));  // (x T alone could leave fp32)
 }
 // max(a, |b|) that keeps a NaN.
 __device__ __forceinline__ float max_abs_nan(float a, float b) {

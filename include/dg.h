@@ -427,8 +427,10 @@ int dg_mx4_matmul(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w,
 /* gelu in its tanh form.  z_in, z_out: device bf16 [rows, d]; w1, w1_scales:*/
 /* W1 transposed, [d_ff, d] as dg_mx4_quantize writes it; w2, w2_scales: W2  */
 /* transposed, [d, d_ff].  z_out may be z_in.  d, d_ff multiples of 64 in    */
-/* [64, 16384].  Workspace: dg_ffw_mx4_workspace_size bytes, 256-byte        */
-/* aligned, any contents.  Three launches, two up to 16 rows.                */
+/* [64, 16384].  Products are summed in fp32: a sum of z_in W1 that leaves it, */
+/* on either side, makes its block of 32 hidden values NaN.  Workspace:       */
+/* dg_ffw_mx4_workspace_size bytes, 256-byte aligned, any contents.  Three    */
+/* launches, two up to 16 rows.                                              */
 /* ------------------------------------------------------------------------ */
 size_t dg_ffw_mx4_workspace_size(int32_t rows, int32_t d, int32_t d_ff);
 

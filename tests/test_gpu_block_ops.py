@@ -424,6 +424,43 @@ def test_block(R, d, dff):
     assert torch.equal(dg.dg_ffw_mx4(zin, w1, w2, out=zin), got)
 
 
+# One to 16 rows, up to 128, pairs of CTAs with 128 and with 256 columns (the kernel's forms of the gelu).
+@pytest.mark.parametrize("R", [1, 16, 100, 300, 20000])
+def test_block_gelu_far_below_zero(R):
+    # With the identity as the second matrix the block returns its quantised hidden layer, exactly; one
+    # nonzero input and one weight per column make every pre-activation a known product of powers of two
+    # and 1, 1.5 or 2.25.  gelu's factor 1 / (1 + e^(2u)) is known to 3 U of its exponent (at most 126
+    # powers of two) plus ex2's 2^-22, 2e-5 together: no value below lies so near a midpoint of the grid.
+    # Products are summed in fp32: one past 2^128 (here -2^90 times 2^57 or 2^63) is infinite, its block NaN.
+    d = dff = 128
+    mixed = [3.0, -6.0, -8.0, -1.0, 0.5, -12.0, -1.5 * 2.0 ** 33, -1.0 * 2.0 ** 60, -1.5 * 2.0 ** 66, 2.0, -4.0, -(2.0 ** 90)]
+    far = [-(2.0 ** 60), -1.5 * 2.0 ** 66, -1e10]
+    # blocks of far values only, of both kinds, and of huge ones
+    v = torch.tensor([-8.0] * 32 + [-6.0] * 32 + (mixed * 3)[:32] + (far * 11)[:32], dtype=torch.float64, device=DEV)
+    W1 = torch.zeros(dff, d, dtype=torch.float64, device=DEV)
+    W1[:, 0] = v
+    w1, w2 = ref.mx4_pack(*ref.mx4_quantize(W1)), ref.mx4_pack(*ref.mx4_quantize(torch.eye(d, device=DEV)))
+    v = ref.mx4_values(*ref.mx4_quantize(W1))[:, 0]
+    factors = torch.tensor([1.0, 0.75, 1.5, 2.0, 2.0 ** 32, 2.0 ** 57, 2.0 ** 63, 0.0, -1.5 * 2.0 ** 30], dtype=torch.float64, device=DEV)
+    factors = factors.repeat(-(-R // 9))[:R]
+    z = torch.zeros(R, d, dtype=BF16, device=DEV)
+    z[:, 0] = factors.to(BF16)
+    x = (factors[:, None] * v).float().double()
+    u2 = 2 * (2 / math.pi) ** 0.5 * (x + 0.044715 * x ** 3)
+    h = x / (1 + torch.exp(-u2))
+    assert torch.equal(h.isnan().any(1), factors.abs() * 2.0 ** 90 >= 2.0 ** 128)
+    a = (h.abs().reshape(R, -1, 32) / torch.exp2(ref.mx4_scale_exponents(h))[..., None]).nan_to_num(0.0)
+    mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64, device=DEV)
+    assert ((a[..., None] / mids - 1).abs() > 2e-5).all()
+    top = a.amax(2)
+    assert ((top == 0) | ((top > 4.001) & (top < 7.999)) | (top < 3.999)).all()  # (the last: at the smallest scale)
+    want = ref.mx4_values(*ref.mx4_quantize(h)).to(BF16)
+    want[h.isnan().any(1)] = float("nan")  # a row's sum over its hidden values
+    got = dg.dg_ffw_mx4(z, w1, w2)
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.nan_to_num(), want.nan_to_num()), (got.double() - want.double()).abs().nan_to_num().max()
+
+
 @pytest.mark.parametrize("R", [8, 200])
 def test_block_nan_and_infinite_rows_stay_alone(R):
     g = gen(13)
