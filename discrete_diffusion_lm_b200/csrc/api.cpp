@@ -205,8 +205,8 @@ NormRuns norm_runs(int32_t B, int32_t C, int32_t d, int act_dtype, bool have_gat
     n.B = have_gate ? B : 1;
     n.C = have_gate ? C : B * C;
     const int32_t want = block_norm_runs(n.B, n.C, d, act_dtype == DG_BF16);
-    n.run_rows = (n.C + want - 1) / want;
-    n.runs = (n.C + n.run_rows - 1) / n.run_rows;
+    n.run_rows = (n.C - 1) / want + 1;  // rounded up, for any C below 2^31
+    n.runs = (n.C - 1) / n.run_rows + 1;
     return n;
 }
 

@@ -1039,7 +1039,7 @@ cudaError_t launch_block_norm(const BlockNormParams& p, int act_bf16, int param_
 int32_t block_norm_runs(int32_t B, int32_t C, int32_t d, int act_bf16) {
     const int n_vec = d / (act_bf16 ? 8 : 4);
     const int per_sm = n_vec <= 512 ? kNormCtas : 1;
-    return std::max(1, std::min<int32_t>(per_sm * num_sms() / B, (C + 1) / 2));
+    return std::max(1, std::min<int32_t>(per_sm * num_sms() / B, C / 2 + C % 2));
 }
 
 cudaError_t launch_block_norm_backward(const BlockNormBackwardParams& p, int act_bf16, int param_bf16, cudaStream_t st) {

@@ -151,6 +151,20 @@ def test_sizes(L):
     assert w(8, 1536, 2048, 1, 1) >= 2 * 8 * 2048 * 4
 
 
+def test_backward_workspace_of_the_largest_row_counts(L):
+    # the runs of rows are counted without leaving 32 bits up to B*C = 2^31 - 1: as many as fill the device
+    w = L.dg_block_norm_backward_workspace_size
+    for d, act in ((8, 1), (8, 0), (16384, 0)):
+        full = w(1, 1 << 20, d, act, 0)
+        assert 0 < full <= 2 * 296 * d * 4
+        runs = full // (8 * d)
+        for B, C in ((1, 1 << 30), (1, 2**31 - 296), (1, 2**31 - 295), (1, 2**31 - 2), (1, 2**31 - 1), (3, 715827882)):
+            assert w(B, C, d, act, 0) == full, (B, C)
+            if B == 1:
+                assert w(B, C, d, act, 1) == full, (B, C)
+        assert w(2, 2**30 - 1, d, act, 1) == 2 * (runs // 2) * 8 * d
+
+
 def test_binding_rejects_before_any_call(L):
     x, w, f = torch.zeros(8, 64, dtype=torch.bfloat16), torch.ones(64), torch.zeros(8, 64)
     for call in (lambda: dg.dg_block_norm(x, w), lambda: dg.dg_block_norm_backward(x, x, x, w, rstd_x=torch.zeros(8)),
