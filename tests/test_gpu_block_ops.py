@@ -212,6 +212,19 @@ def test_norm_backward(B, C, d, T, P):
         check_backward(args, C, s, run_backward(args, C), T)
 
 
+# many rows: groups of one, two, four and eight that refill their ring's slots several times over, widths full and
+# not; rows of up to 32 vectors, a group several of them; more than 1024 vectors, several rows to a run; runs and
+# groups that end short
+@pytest.mark.parametrize("T,P", [(BF16, F32), (BF16, BF16), (F32, F32)])
+@pytest.mark.parametrize("B,C,d", [(8, 1536, 2048), (4, 3000, 512), (3, 2500, 1000), (3, 2001, 2056), (5, 3000, 264), (2, 1500, 4096),
+                                   (2, 1200, 8192), (2, 300, 16384), (256, 64, 64), (200, 81, 72)])
+def test_norm_backward_many_rows(B, C, d, T, P):
+    s = torch.tensor(0.7, dtype=F32).item()
+    for mode, gated, with_dx in (("both", True, True), ("both", False, False), ("pre", False, True), ("post", True, True)):
+        args = backward_case(B, C, d, T, P, mode, gated, with_dx=with_dx)
+        check_backward(args, C, s, run_backward(args, C), T)
+
+
 @pytest.mark.parametrize("which", ["x", "y", "w_post", "gate", "w_pre"])
 def test_norm_gradients_against_differences(which):
     # the derivative of a random linear functional of (stream, h) along a random direction, by central
