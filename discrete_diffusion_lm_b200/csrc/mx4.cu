@@ -1059,7 +1059,8 @@ cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
     //    (128 tiles of 64 rows, K = 8192: 17.1, pairs 19.1; 256 tiles, K = 2048: 16.0, pairs 12.8) or four splits
     //    shorten K > 1024 (16 tiles of 17 rows: 5.3, pairs 6.1; 32 tiles of 64 rows, K = 1024: 6.0, pairs 5.2; 64
     //    tiles of 64 rows, two splits: 7.2, pairs 6.7);
-    //  * up to 16 rows single CTAs: their epilogue is as short as the pairs' (8 tiles of a row: 4.7, pairs 4.8).
+    //  * up to kMx4FewRows rows single CTAs, which alone take A as bf16: their epilogue is as short as the pairs' (8
+    //    tiles of a row: 4.7, pairs 4.8).
     const int64_t pairs = static_cast<int64_t>((q.M + 255) / 256) * ((q.N + 127) / 128);
     const int64_t singles = static_cast<int64_t>((q.M + kMTile - 1) / kMTile) * ((q.N + kNTile - 1) / kNTile);
     const int32_t k_blocks = (q.K + kKStage - 1) / kKStage;
@@ -1070,7 +1071,7 @@ cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
     int splits = 1;
     while (splits < 4 && 2 * splits * singles <= (splits == 1 ? num_sms() : 128) && 2 * splits <= k_blocks) splits *= 2;
     const bool paired = q.M > 128 ? splits == 1 || k_blocks <= 8
-                                  : q.M > 16 && (k_blocks <= 4 || (k_blocks <= 8 && splits == 2) || singles > num_sms());
+                                  : q.M > kMx4FewRows && (k_blocks <= 4 || (k_blocks <= 8 && splits == 2) || singles > num_sms());
     if (paired) {
         const bool wide = 2 * pairs > num_sms();
         if (q.out_kind == kMx4OutF32) return wide ? launch_pair<kOutF32, 256>(q, st) : launch_pair<kOutF32, 128>(q, st);
