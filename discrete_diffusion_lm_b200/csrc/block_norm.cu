@@ -531,8 +531,9 @@ cudaError_t forward_by_width(const BlockNormParams& p, cudaStream_t st) {
     if (n_vec <= 256) return launch_rows<T, P, 4, 2, 2, 2>(p, st);
     if (n_vec <= 512) return launch_rows<T, P, 8, 1, 2, 2>(p, st);
     if (n_vec <= 1024) return launch_rows<T, P, 16, 1, 2, 1>(p, st);
-    if (n_vec <= 2048) return launch_forward<T, P, 16, 4>(p, st);
-    return launch_forward<T, P, 32, 4>(p, st);
+    if constexpr (sizeof(T) == 4)  // (bf16 rows have 2048 vectors at most)
+        if (n_vec > 2048) return launch_forward<T, P, 32, 4>(p, st);
+    return launch_forward<T, P, 16, 4>(p, st);
 }
 
 // ------------------------------------------------------------------------------------ backward
