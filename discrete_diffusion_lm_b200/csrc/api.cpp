@@ -1013,6 +1013,17 @@ int dg_test_mx4_stall(const uint8_t* a, const uint8_t* a_scales, const uint8_t* 
     return mx4_matmul_impl(a, a_scales, w, w_scales, M, N, K, out, out_dtype, stream, stalled_block, static_cast<long long>(limit_cycles));
 }
 
+int dg_test_mx4_plan(int32_t M, int32_t N, int32_t K, int32_t* splits, int32_t* columns) {
+    g_last_error.clear();
+    int rc;
+    if (!splits || !columns) return fail(DG_ERR_INVALID_ARG, "splits and columns are required");
+    if ((rc = check_mx4_matrix(M, K)) != DG_OK || (rc = check_mx4_matrix(N, K)) != DG_OK) return rc;
+    const Mx4Plan plan = mx4_plan(M, N, K);
+    *splits = plan.splits;
+    *columns = plan.columns;
+    return DG_OK;
+}
+
 size_t dg_ffw_mx4_workspace_size(int32_t rows, int32_t d, int32_t d_ff) {
     if (rows < 1 || d < 64 || d_ff < 64) return 0;
     return ffw_mx4_parts(rows, d, d_ff).total;

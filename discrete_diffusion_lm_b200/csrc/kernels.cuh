@@ -198,6 +198,11 @@ struct Mx4MatmulParams {
     long long wait_limit;  // test hook: cycles a wait may last (0: the default) ...
     int32_t fault_block;   // ... and the 256-value block of K whose copies are then never issued
 };
+struct Mx4Plan {
+    int32_t splits;   // single CTAs, K split over so many of a cluster; 0: pairs of CTAs
+    int32_t columns;  // of a tile
+};
+Mx4Plan mx4_plan(int32_t M, int32_t N, int32_t K);
 cudaError_t launch_mx4_matmul(const Mx4MatmulParams& p, cudaStream_t s);
 cudaError_t read_and_clear_mx4_error(int* out);
 cudaError_t read_and_clear_norm_error(int* out);

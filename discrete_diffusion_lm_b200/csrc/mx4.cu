@@ -1049,7 +1049,7 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
     return cudaGetLastError();
 }
 
-cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
+Mx4Plan mx4_plan(int32_t M, int32_t N, int32_t K) {
     // Which kernel, from sizes alone (us a product, K = 2048 unless said):
     //  * more 256 x 128 tiles than pairs: 256 x 256 tiles (96 tiles: 8.6, with 128 columns 10.2, single
     //    CTAs 14.7; a block on 4096 rows of 2048: 70, with 128 columns 83);
@@ -1061,23 +1061,30 @@ cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
     //    tiles of 64 rows, two splits: 7.2, pairs 6.7);
     //  * up to kMx4FewRows rows single CTAs, which alone take A as bf16: their epilogue is as short as the pairs' (8
     //    tiles of a row: 4.7, pairs 4.8).
-    const int64_t pairs = static_cast<int64_t>((q.M + 255) / 256) * ((q.N + 127) / 128);
-    const int64_t singles = static_cast<int64_t>((q.M + kMTile - 1) / kMTile) * ((q.N + kNTile - 1) / kNTile);
-    const int32_t k_blocks = (q.K + kKStage - 1) / kKStage;
+    const int64_t pairs = static_cast<int64_t>((M + 255) / 256) * ((N + 127) / 128);
+    const int64_t singles = static_cast<int64_t>((M + kMTile - 1) / kMTile) * ((N + kNTile - 1) / kNTile);
+    const int32_t k_blocks = (K + kKStage - 1) / kKStage;
     // single CTAs: split K while the clusters fit one wave and every split keeps a block.  (Clusters of
     // eight are placed two to a GPC at most: 200 x 1000 x 4096 took 10.8 us split in eight, 7.5 in four.  GPCs
     // hold unequal numbers of SMs, so not all 148 take clusters of four: 33 tiles in four splits, K = 6624, 100
     // rows, 9.8 us, 34 tiles 16.1, and 38 in two 11.3.  Every GPC of 16 SMs or more has room for four.)
     int splits = 1;
     while (splits < 4 && 2 * splits * singles <= (splits == 1 ? num_sms() : 128) && 2 * splits <= k_blocks) splits *= 2;
-    const bool paired = q.M > 128 ? splits == 1 || k_blocks <= 8
-                                  : q.M > kMx4FewRows && (k_blocks <= 4 || (k_blocks <= 8 && splits == 2) || singles > num_sms());
-    if (paired) {
-        const bool wide = 2 * pairs > num_sms();
+    const bool paired = M > 128 ? splits == 1 || k_blocks <= 8
+                                : M > kMx4FewRows && (k_blocks <= 4 || (k_blocks <= 8 && splits == 2) || singles > num_sms());
+    if (paired) return {0, 2 * pairs > num_sms() ? 256 : 128};
+    return {splits, kNTile};
+}
+
+cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
+    const Mx4Plan plan = mx4_plan(q.M, q.N, q.K);
+    if (plan.splits == 0) {
+        const bool wide = plan.columns == 256;
         if (q.out_kind == kMx4OutF32) return wide ? launch_pair<kOutF32, 256>(q, st) : launch_pair<kOutF32, 128>(q, st);
         if (q.out_kind == kMx4OutBf16) return wide ? launch_pair<kOutBf16, 256>(q, st) : launch_pair<kOutBf16, 128>(q, st);
         return wide ? launch_pair<kOutGeluMx4, 256>(q, st) : launch_pair<kOutGeluMx4, 128>(q, st);
     }
+    const int splits = plan.splits;
     Mx4Kernel kp;
     std::memset(&kp, 0, sizeof(kp));
     cudaError_t e = cudaSuccess;
@@ -1095,10 +1102,10 @@ cudaError_t launch_mx4_matmul(const Mx4MatmulParams& q, cudaStream_t st) {
     kp.K = q.K;
     kp.n_tiles = (q.N + kNTile - 1) / kNTile;
     kp.k_tiles = (q.K + 127) / 128;
-    kp.k_blocks = k_blocks;
+    kp.k_blocks = (q.K + kKStage - 1) / kKStage;
     kp.wait_limit = q.wait_limit > 0 ? q.wait_limit : kWaitLimitCycles;
     kp.fault_block = q.wait_limit > 0 ? q.fault_block : -1;
-    const int64_t grid = singles * splits;
+    const int64_t grid = static_cast<int64_t>((q.M + kMTile - 1) / kMTile) * kp.n_tiles * splits;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
     if (q.out_kind == kMx4OutF32) return launch_product<kOutF32>(kp, static_cast<int>(grid), splits, q.dependent != 0, st);
     if (q.out_kind == kMx4OutBf16) return launch_product<kOutBf16>(kp, static_cast<int>(grid), splits, q.dependent != 0, st);

@@ -54,6 +54,9 @@ int dg_test_selfcond_stall(const void* logits, int logits_dtype, int64_t ld, int
 /*   every wait limited to limit_cycles: the CTAs give up, wait for their   */
 /*   copies in flight, free their tensor memory and return; out is then     */
 /*   incomplete.                                                            */
+/* dg_test_mx4_plan: which kernel dg_mx4_matmul takes for these sizes: the   */
+/*   CTAs of a cluster that K is split over (1, 2 or 4), or 0 for pairs of   */
+/*   CTAs, and the columns of a tile.  Host only.                            */
 /* dg_test_block_norm_stall: dg_block_norm before a block (x contiguous, no  */
 /*   y, eps 1e-6) with row 0 never fetched and every wait limited to limit_cycles,     */
 /*   where the call is of the form that keeps rows in flight (many rows, at  */
@@ -63,6 +66,8 @@ int dg_test_mx4_stall(const uint8_t* a, const uint8_t* a_scales, const uint8_t* 
                       const uint8_t* w_scales, int32_t M, int32_t N, int32_t K, void* out,
                       int out_dtype, dg_stream_t stream, int32_t stalled_block,
                       uint32_t limit_cycles);
+
+int dg_test_mx4_plan(int32_t M, int32_t N, int32_t K, int32_t* splits, int32_t* columns);
 
 int dg_test_block_norm_stall(const void* x, int act_dtype, const void* w_pre, int param_dtype,
                              int32_t rows, int32_t d, void* h, uint32_t limit_cycles,

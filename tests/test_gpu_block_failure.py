@@ -33,6 +33,18 @@ def test_product_stall(M, N, K, block):
     assert torch.equal(dg.dg_mx4_matmul(a, w), want)
 
 
+# the same with the kernel that each size is meant for: (CTAs that share K, or 0 for pairs; columns of a tile)
+@pytest.mark.parametrize("M,N,K,block,plan", [
+    (16, 128, 256, 0, (1, 128)), (1, 8192, 2048, 2, (2, 128)), (1, 8192, 2048, 5, (2, 128)), (100, 4864, 6624, 15, (2, 128)),
+    (200, 2432, 6624, 4, (2, 128)), (5, 512, 4096, 9, (4, 128)), (100, 1024, 6624, 25, (4, 128)),
+    (200, 4096, 2048, 7, (0, 128)), (2048, 4096, 1024, 3, (0, 256))])
+def test_product_stall_of_every_kernel(M, N, K, block, plan):
+    got = torch.zeros(2, dtype=torch.int32)
+    assert dg.lib().dg_test_mx4_plan(M, N, K, got[0:].data_ptr(), got[1:].data_ptr()) == 0
+    assert tuple(got.tolist()) == plan
+    test_product_stall(M, N, K, block)
+
+
 @pytest.mark.parametrize("rows,d", [(1500, 128), (2000, 512), (1400, 2048), (1300, 4096)])
 def test_norm_stall(rows, d):
     g = torch.Generator(device=DEV).manual_seed(2)
