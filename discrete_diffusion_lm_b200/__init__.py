@@ -124,6 +124,7 @@ def lib() -> ctypes.CDLL:
         L.dg_test_mx4_stall.argtypes = [_p, _p, _p, _p, _i32, _i32, _i32, _p, _int, _p, _i32, _u32]
         L.dg_test_mx4_plan.argtypes = [_i32, _i32, _i32, _p, _p]
         L.dg_test_block_norm_stall.argtypes = [_p, _int, _p, _int, _i32, _i32, _p, _u32, _p]
+        L.dg_test_block_norm_backward_stall.argtypes = [_p, _p, _int, _p, _int, _i32, _i32, _p, _p, _p, _p, _sz, _u32, _p]
         L.dg_ffw_mx4_workspace_size.argtypes = [_i32, _i32, _i32]
         L.dg_ffw_mx4_workspace_size.restype = _sz
         L.dg_ffw_mx4.argtypes = [_p, _i32, _i32, _i32, _p, _p, _p, _p, _p, _p, _sz, _p]

@@ -864,11 +864,14 @@ size_t dg_block_norm_backward_workspace_size(int32_t B, int32_t C, int32_t d, in
     return 2 * static_cast<size_t>(n.B) * n.runs * d * sizeof(float);
 }
 
-int dg_block_norm_backward(const void* dx_out, int64_t ld_dx_out, const void* dh, int64_t ld_dh, const void* x, int64_t ld_x,
-                           const void* y, int64_t ld_y, int act_dtype, const void* w_post, const void* gate,
-                           const void* w_pre, int param_dtype, int32_t B, int32_t C, int32_t d, float res_scale,
-                           const float* rstd_y, const float* rstd_x, void* dx, void* dy, float* dw_post, float* dgate,
-                           float* dw_pre, void* workspace, size_t workspace_bytes, dg_stream_t stream) {
+}  // extern "C"
+
+namespace {
+int block_norm_backward_impl(const void* dx_out, int64_t ld_dx_out, const void* dh, int64_t ld_dh, const void* x, int64_t ld_x,
+                             const void* y, int64_t ld_y, int act_dtype, const void* w_post, const void* gate,
+                             const void* w_pre, int param_dtype, int32_t B, int32_t C, int32_t d, float res_scale,
+                             const float* rstd_y, const float* rstd_x, void* dx, void* dy, float* dw_post, float* dgate,
+                             float* dw_pre, void* workspace, size_t workspace_bytes, dg_stream_t stream, long long wait_limit) {
     g_last_error.clear();
     int rc;
     if ((rc = check_norm_shape(act_dtype, param_dtype, B, C, d, res_scale)) != DG_OK) return rc;
@@ -925,9 +928,33 @@ int dg_block_norm_backward(const void* dx_out, int64_t ld_dx_out, const void* dh
     p.dw_pre = dw_pre;
     p.part_pre = static_cast<float*>(workspace);
     p.part_post = p.part_pre + static_cast<size_t>(n.B) * n.runs * d;
+    p.wait_limit = wait_limit;
     const cudaError_t e = launch_block_norm_backward(p, act_dtype == DG_BF16, param_dtype == DG_BF16, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "block norm backward launch");
     return DG_OK;
+}
+}  // namespace
+
+extern "C" {
+
+int dg_block_norm_backward(const void* dx_out, int64_t ld_dx_out, const void* dh, int64_t ld_dh, const void* x, int64_t ld_x,
+                           const void* y, int64_t ld_y, int act_dtype, const void* w_post, const void* gate,
+                           const void* w_pre, int param_dtype, int32_t B, int32_t C, int32_t d, float res_scale,
+                           const float* rstd_y, const float* rstd_x, void* dx, void* dy, float* dw_post, float* dgate,
+                           float* dw_pre, void* workspace, size_t workspace_bytes, dg_stream_t stream) {
+    return block_norm_backward_impl(dx_out, ld_dx_out, dh, ld_dh, x, ld_x, y, ld_y, act_dtype, w_post, gate, w_pre, param_dtype,
+                                    B, C, d, res_scale, rstd_y, rstd_x, dx, dy, dw_post, dgate, dw_pre, workspace,
+                                    workspace_bytes, stream, 0);
+}
+
+int dg_test_block_norm_backward_stall(const void* dh, const void* x, int act_dtype, const void* w_pre, int param_dtype, int32_t rows,
+                                      int32_t d, const float* rstd_x, void* dx, float* dw_pre, void* workspace,
+                                      size_t workspace_bytes, uint32_t limit_cycles, dg_stream_t stream) {
+    g_last_error.clear();
+    if (limit_cycles == 0) return fail(DG_ERR_INVALID_ARG, "limit_cycles must be > 0");
+    return block_norm_backward_impl(nullptr, d, dh, d, x, d, nullptr, d, act_dtype, nullptr, nullptr, w_pre, param_dtype, 1, rows, d,
+                                    1.0f, nullptr, rstd_x, dx, nullptr, nullptr, nullptr, dw_pre, workspace, workspace_bytes, stream,
+                                    static_cast<long long>(limit_cycles));
 }
 
 size_t dg_mx4_scale_bytes(int32_t rows, int32_t K) { return rows < 1 || K < 1 ? 0 : mx4_scale_bytes(rows, K); }

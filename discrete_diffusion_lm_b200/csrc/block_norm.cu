@@ -714,7 +714,8 @@ __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
         next += slots * kGroups;
         ++fills;
     };
-    if (kRing && t < ahead) fetch(t);
+    // (the test hook leaves the first row out)
+    if (kRing && t < ahead && !(p.wait_limit > 0 && blockIdx.x == 0 && threadIdx.x == 0)) fetch(t);
     uint4 row[kAhead][4];
     const auto load_row = [&](int i, uint4(&v)[4]) {
         const int64_t r = r0 + static_cast<int64_t>(i) * kGroups;

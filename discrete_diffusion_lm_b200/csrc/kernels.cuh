@@ -166,7 +166,7 @@ struct BlockNormBackwardParams {
     void *dx, *dy;             // [R, d]
     float *dw_post, *dgate, *dw_pre;
     float *part_pre, *part_post;  // [B * runs, d] partial sums
-    long long wait_limit;         // cycles a wait may last (0: the default)
+    long long wait_limit;         // test hook: cycles a wait may last, and row 0 is never fetched (0: the default)
 };
 int32_t block_norm_runs(int32_t B, int32_t C, int32_t d, int act_bf16);
 cudaError_t launch_block_norm_backward(const BlockNormBackwardParams& p, int act_bf16, int param_bf16, cudaStream_t s);

@@ -62,6 +62,10 @@ int dg_test_selfcond_stall(const void* logits, int logits_dtype, int64_t ld, int
 /*   where the call is of the form that keeps rows in flight (many rows, at  */
 /*   most 1024 16-byte vectors wide); h of the rows walked with it is then   */
 /*   meaningless.                                                            */
+/* dg_test_block_norm_backward_stall: dg_block_norm_backward of the same     */
+/*   norm (no dx_out, no y) with the first row never fetched, where the call */
+/*   keeps rows in flight (33 to 1024 16-byte vectors wide); dx of the rows  */
+/*   walked with it and dw_pre are then meaningless.                         */
 int dg_test_mx4_stall(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w,
                       const uint8_t* w_scales, int32_t M, int32_t N, int32_t K, void* out,
                       int out_dtype, dg_stream_t stream, int32_t stalled_block,
@@ -72,6 +76,11 @@ int dg_test_mx4_plan(int32_t M, int32_t N, int32_t K, int32_t* splits, int32_t* 
 int dg_test_block_norm_stall(const void* x, int act_dtype, const void* w_pre, int param_dtype,
                              int32_t rows, int32_t d, void* h, uint32_t limit_cycles,
                              dg_stream_t stream);
+
+int dg_test_block_norm_backward_stall(const void* dh, const void* x, int act_dtype, const void* w_pre,
+                                      int param_dtype, int32_t rows, int32_t d, const float* rstd_x,
+                                      void* dx, float* dw_pre, void* workspace, size_t workspace_bytes,
+                                      uint32_t limit_cycles, dg_stream_t stream);
 
 #ifdef __cplusplus
 }

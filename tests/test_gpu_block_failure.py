@@ -59,8 +59,35 @@ def test_norm_stall(rows, d):
     assert dg.dg_device_error() == 0
 
 
+# the gradients: groups of one, two, four and eight; walks of several times the ring's slots, and one that fits them
+@pytest.mark.parametrize("rows,d", [(30000, 512), (20000, 1024), (9000, 2048), (5000, 4096), (2500, 8192), (500, 1000)])
+def test_norm_backward_stall(rows, d):
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x, dh = (torch.randn(rows, d, generator=g, device=DEV).bfloat16() for _ in range(2))
+    w = torch.randn(d, generator=g, device=DEV)
+    rstd = dg.dg_block_norm(x, w)["rstd_x"]
+    want = dg.dg_block_norm_backward(None, dh, x, w, rstd_x=rstd)
+    assert dg.dg_device_error() == 0
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    ws = torch.empty(dg.lib().dg_block_norm_backward_workspace_size(1, rows, d, dg.DG_BF16, 0), dtype=torch.uint8, device=DEV)
+    rc = dg.lib().dg_test_block_norm_backward_stall(dh.data_ptr(), x.data_ptr(), dg.DG_BF16, w.data_ptr(), dg.DG_F32, rows, d, rstd.data_ptr(),
+                                                    dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), ws.numel(), LIMIT, stream())
+    assert rc == 0, dg.dg_last_error()
+    assert dg.dg_device_error() == 1
+    assert torch.equal(dx[rows // 2:], want["dx"][rows // 2:])  # rows that other CTAs walk are as ever
+    again = dg.dg_block_norm_backward(None, dh, x, w, rstd_x=rstd, ws=ws)
+    assert all(torch.equal(again[k], want[k]) for k in want)
+    assert dg.dg_device_error() == 0
+
+
 def test_hooks_refuse():
     L = dg.lib()
     assert L.dg_test_mx4_stall(*[1 << 20] * 4, 16, 128, 256, 1 << 20, 1, None, -1, 100) == 1
     assert L.dg_test_mx4_stall(*[1 << 20] * 4, 16, 128, 256, 1 << 20, 1, None, 0, 0) == 1
     assert L.dg_test_block_norm_stall(1 << 20, 1, 1 << 20, 1, 8, 64, 1 << 21, 0, None) == 1
+
+
+def test_backward_hook_refuses():
+    a = 1 << 20
+    assert dg.lib().dg_test_block_norm_backward_stall(a, a, 1, a, 1, 8, 64, a, 2 * a, a, a, 1 << 20, 0, None) == 1
+    assert dg.lib().dg_test_block_norm_backward_stall(a, a, 1, a, 1, 8, 64, a, 2 * a, a, a, 0, 100, None) == 3
