@@ -396,9 +396,10 @@ int dg_block_norm_backward(const void* dx_out, int64_t ld_dx_out, const void* dh
 /*   6 to 6).  A block with a NaN or an infinity gets c = 255.  x: device    */
 /*   DG_F32 or DG_BF16 [rows, K], row stride ld >= K, base and stride        */
 /*   multiples of 16 bytes.  Writes codes and every byte of scales.          */
-/* dg_mx4_dequantize: the values, as DG_F32 (exact; subnormal results are    */
-/*   kept) or DG_BF16 (exact except where 2^(c-127) leaves its range) in out */
-/*   [rows, K], contiguous.                                                  */
+/* dg_mx4_dequantize: the values, as DG_F32 or DG_BF16, in out [rows, K],     */
+/*   contiguous.  Exact, subnormal results too, except that the scale bytes  */
+/*   253 and 254, which dg_mx4_quantize never writes, take the values past   */
+/*   either type's range (2^128 and more) to infinity.                       */
 /* K <= 2^24, rows <= 2^31 - 256.  All pointers 16-byte aligned, nothing      */
 /* aliased, no workspace, one launch.                                        */
 /* ------------------------------------------------------------------------ */
