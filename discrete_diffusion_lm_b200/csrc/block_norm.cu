@@ -10,6 +10,9 @@
 //   dw_pre = sum_r dh m,  P_b = sum_{r in b} dx v,  dw_post = s sum_b g_b P_b,  dgate_b = s w_post P_b.
 // Sums, statistics and everything between a load and a store are fp32; x', h, dx and dy are rounded
 // once, to the activations' type (h is taken of the unrounded x').
+//
+// Times below are of launches back to back in one graph that rotate over inputs and outputs of 500 MB together,
+// so that rows come from memory; those marked [L2] rotate over four sets, which L2 holds where they are small.
 #include <algorithm>
 
 #include "common.cuh"
@@ -139,8 +142,8 @@ __device__ __forceinline__ float row_rstd(const float (&f)[kNV][kN], float inv_d
 // One row per group of kWarps warps, kNV 16-byte vectors per thread, everything in registers: each
 // input is read once.  kWarps == 1: four rows per CTA, no barrier; else one row per CTA.  Every step is
 // rounded as in the ring below, so that a row's results do not depend on the number of rows.  Few rows cost
-// the launch and one trip to memory (64 x 256 bf16: 2.2 us); a row too wide for the ring is bound by the
-// two sums that stand between its loads and its stores (512 x 16384 fp32: 33.6 us, 4.0 TB/s).
+// the launch and one trip to memory (64 x 256 bf16: 2.4 us); a row too wide for the ring is bound by the
+// two sums that stand between its loads and its stores (512 x 16384 fp32: 30.9 us, 4.3 TB/s).
 template <typename T, typename P, int kWarps, int kNV>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) block_norm_kernel(const __grid_constant__ BlockNormParams p) {
     constexpr int kN = Vec<T>::kN;
@@ -223,10 +226,10 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : 32 * kWarps) block_norm_ke
 // shared-memory slots with a barrier each.  Beside memory it is instructions that bound such a
 // walk, so the parameters stay in registers, as fp32 pairs for the packed fma.rn.f32x2, and widths
 // that fill every thread's vectors (kFull) have no column checks.  A CTA has kGroups groups, each with
-// its own ring and named barrier.  bf16, both norms with a gate, 2048 columns: 256 rows 3.3 us, 4096 rows
-// 13.9 us (4.8 TB/s), 12288 rows 36.9 us (5.5 TB/s); without the packed arithmetic and with ordinary loads 4096
-// rows took 18 us.  Two CTAs an SM: three, with 80 registers a
-// thread, were no faster.
+// its own ring and named barrier.  bf16, both norms with a gate, 2048 columns: 256 rows 3.9 us, 4096 rows
+// 15.6 us (4.3 TB/s: 7 rows a group barely fill the ring once, and the loads' latency bounds it), 12288 rows
+// 38.0 us (5.3 TB/s).  Without the packed arithmetic and with ordinary loads 4096 rows took 18 us where this takes
+// 13.7 [L2].  Two CTAs an SM: three, with 80 registers a thread, were no faster.
 template <typename T, int kP>
 __device__ __forceinline__ void unpack_pairs(const uint4& v, Pair (&p)[kP]) {
     float f[2 * kP];
@@ -519,10 +522,10 @@ template <typename T, typename P>
 cudaError_t forward_by_width(const BlockNormParams& p, cudaStream_t st) {
     const int n_vec = p.d / Vec<T>::kN;
     // Which form (us, bf16, both norms with a gate).  Up to 32 vectors a warp has a row, and the direct form's
-    // one load per thread is all there is to wait for (256 columns, 64, 4096 and 16384 rows: 2.3, 2.9, 7.0;
-    // the ring 2.6, 3.7, 8.3) until the rows are so many that memory is (65536 rows: 28.6, ring 22.6).  Wider,
-    // the ring, at any number of rows (2048 columns, 64, 4096 and 16384 rows: 2.7, 11.4, 43.6; direct 3.2,
-    // 14.9, 54.4), as long as the parameters of a thread's columns fit its registers and three rows the
+    // one load per thread is all there is to wait for (256 columns, 64, 4096 and 16384 rows: 2.4, 4.3, 10.8;
+    // the ring 2.9, 5.3, 10.5) until the rows are so many that memory is (65536 rows: 33.7, ring 27.6).  Wider,
+    // the ring, at any number of rows (2048 columns, 64, 4096 and 16384 rows: 3.0, 15.6, 52.1; direct 3.3,
+    // 19.4, 63.4), as long as the parameters of a thread's columns fit its registers and three rows the
     // shared memory.  (The test hook's bounded waits are the ring's.)
     if (n_vec <= 32 && p.R < 256 * num_sms() && p.wait_limit <= 0) return launch_forward<T, P, 1, 1>(p, st);
     if (n_vec <= 32) return launch_rows<T, P, 1, 8, 1, 3>(p, st);
@@ -669,11 +672,11 @@ __device__ __forceinline__ void store_pairs(float* to, Pair a, Pair b) {
 
 // The same with the rows' bulk copies kept in flight (see block_norm_rows_kernel).  A CTA's rows are of
 // one canvas; its groups take them in turn, and their columns' sums are added at the end, in the
-// order of the groups.  12288 x 2048 bf16, gated: 61.9 us with the sums below (4.9 TB/s);
+// order of the groups.  12288 x 2048 bf16, gated: 61.4 us with the sums below (4.9 TB/s);
 // an instruction is issued in 59 % of the cycles, so arithmetic and the exchange of a row's sums bound it as
-// much as memory (55 % busy).  1024 x 4096 fp32: 26 us, read twice as above 31.  Rows of up to 32 vectors are
-// too small for bulk copies (four of 128 bytes a row: 16384 x 64 bf16 took 19.3 us) and come by loads two rows ahead
-// (14.0 us; three spill).
+// much as memory (55 % busy).  1024 x 4096 fp32: 25.5 us, read twice as above 31.  Rows of up to 32 vectors are
+// too small for bulk copies (four of 128 bytes a row: 16384 x 64 bf16 took 19.3 us [L2]) and come by loads two rows ahead
+// (14.0 [L2], from memory 19.2; three spill).
 template <typename T, typename P, int kW, int kGroups, int kNV, int kCtas, bool kFull>
 __global__ void __launch_bounds__(32 * kW * kGroups, kCtas)
     block_norm_backward_rows_kernel(const __grid_constant__ BlockNormBackwardParams p, int slots) {
@@ -968,7 +971,7 @@ cudaError_t launch_params(const BlockNormBackwardParams& p, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     // With one canvas to a lane and more CTAs than the SMs hold at 96 registers, the form of 40 (1024 x 8192 fp32 in
-    // four canvases: 60.5 us, else 63.7; with fewer CTAs it is the slower one, 4096 x 1024 in 16: 22.2 and 19.6).
+    // four canvases: 60.5 us, else 63.7; with fewer CTAs it is the slower one, 4096 x 1024 in 16: 22.2 and 19.6 [L2]).
     e = sub > 1 && static_cast<int>(cfg.gridDim.x * cfg.gridDim.y) > 2 * num_sms()
             ? cudaLaunchKernelEx(&cfg, block_norm_params_kernel<P, 1>, p, sub)
             : cudaLaunchKernelEx(&cfg, block_norm_params_kernel<P, 4>, p, sub);
@@ -1037,7 +1040,7 @@ cudaError_t launch_block_norm(const BlockNormParams& p, int act_bf16, int param_
 }
 
 // Runs of rows per canvas: as many CTAs as the SMs hold at once, but two rows to a run, so that there
-// are not more partial sums than need be (256 rows of 2048 in runs of one, two, four: 11.9, 9.4, 9.8 us).
+// are not more partial sums than need be (256 rows of 2048 in runs of one, two, four: 11.9, 9.4, 9.8 us [L2]).
 int32_t block_norm_runs(int32_t B, int32_t C, int32_t d, int act_bf16) {
     const int n_vec = d / (act_bf16 ? 8 : 4);
     const int per_sm = n_vec <= 512 ? kNormCtas : 1;

@@ -183,8 +183,8 @@ enum Mx4OutKind : int {
     kMx4OutGelu = 2,  // gelu of the product, quantised again
 };
 // Up to so many rows the product quantises a bf16 A itself (a block of 1024 x 4096 x 1024 on one row called from
-// Python, which takes longer than the GPU: 16.0 us, with a launch for the quantisation 19.3; captured, where the
-// launch costs little and the products start beside it: 11.7 and 10.7).  Beyond, every column tile's doing it
+// Python, which takes longer than the GPU: 16.0 us, with a launch for the quantisation 19.3; captured on weights
+// that L2 holds, where the launch costs little and the products start beside it: 11.7 and 10.7).  Beyond, every column tile's doing it
 // again costs more than the launch (2048 x 8192 x 2048 on 32 rows: 17.0 and 16.2).
 constexpr int32_t kMx4FewRows = 16;
 struct Mx4MatmulParams {

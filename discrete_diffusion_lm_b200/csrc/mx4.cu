@@ -10,6 +10,9 @@
 // Scale bytes lie as the tensor core takes them: tiles of 128 rows x 4 blocks (128 values), 512
 // bytes, byte (r % 32) * 16 + (r / 32 % 4) * 4 + block % 4; tiles of one row group are consecutive.
 // Padding in a tile (rows or blocks past the matrix) holds 127.
+//
+// Times below are of launches back to back in one graph that rotate over inputs and outputs of 500 MB together;
+// those marked [L2], the rules' among them, rotate over three or four sets, which L2 mostly holds.
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 
@@ -65,7 +68,7 @@ __device__ __forceinline__ uint16_t pack_e2m1(const float (&f)[4], float inv) {
 // ------------------------------------------------------------------------------------ quantisation
 // Both directions are bound by memory.  A warp takes kMx4Cols columns of a row: vectors of 16 bytes per
 // lane, contiguous over the warp (4 fp32 or 8 bf16 values), all loaded before the first is used; a
-// block of 32 lies in 8 or 4 lanes.  8192 x 2048 fp32 takes 15.4 us (4.9 TB/s), and 14.8 us back.
+// block of 32 lies in 8 or 4 lanes.  8192 x 2048 fp32 takes 16.0 us (4.7 TB/s), and 15.1 us back.
 constexpr int kMx4Cols = 512;
 
 __device__ __forceinline__ uint8_t* scale_word(uint8_t* scales, int32_t r, int32_t k_tiles, int32_t k) {
@@ -192,8 +195,8 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* __re
 // each stage of it into shared memory, a block of 32 values per thread, in the place of its copies.
 // With few tiles K is split over the CTAs of a cluster: each sends every other its share of the rows
 // of its fp32 tile (bulk copies into that CTA's inbox), and adds the shares it is sent in a fixed order.
-// Few rows cost latency, not bandwidth: 1 x 8192 x 2048 (8.9 MB of W) takes 7.0 us, 1 x 2048 x 8192 6.9 (without
-// the split 13.0).
+// Few rows cost latency, not bandwidth: 1 x 8192 x 2048 (8.9 MB of W) takes 7.6 us, 1 x 2048 x 8192 8.3 (6.9
+// [L2], without the split 13.0 [L2]).
 constexpr int kMTile = 128, kNTile = 128, kKStage = 256;
 constexpr int kMx4Threads = 384;  // W copies, products, A copies, scale copies; eight epilogue warps
 constexpr uint32_t kOperandBytes = 128 * kKStage / 2;
@@ -271,11 +274,11 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // GELU, tanh form, as x T / (1 + T) with T = exp(2u), two values at a time.  The hidden layer is rounded to 4
 // bits by comparisons with the E2M1 midpoints, so an error here moves values across them: the hardware
 // tanh's 2^-11 would move one value in a few hundred, ex2 and a reciprocal (about 2^-22) one in a
-// million.  The special-function unit bounds the epilogue (without the gelu a block on 4096 rows of 1024 x
-// 4096 takes 27 us), so two values share a reciprocal: 1 / a = b (1 / ab); 31.8 us, with one each 32.6, with
+// million.  The special-function unit bounds the epilogue (a block on 4096 rows of 1024 x 4096 takes 32.1 us,
+// without the gelu 26.7), so two values share a reciprocal: 1 / a = b (1 / ab); with one each 33.8 us, with
 // Newton's iteration instead no less.  T is kept below 2^62, so that ab and its reciprocal are normal numbers (from
 // 2^24 on T / (1 + T) is 1 anyway); below, T goes to zero as it should, at 2^-126.  A sum that left fp32 gives no
-// number on either side; taking -infinity for 0, two instructions more for each pair, cost 1.7 us.
+// number on either side; taking -infinity for 0, two instructions more for each pair, cost 0.9 us.
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -627,9 +630,11 @@ cudaError_t launch_product(const Mx4Kernel& kp, int grid, int splits, bool depen
 // thread commits a stage to both CTAs' empty barriers and a finished tile to both accumulator
 // barriers.  256 accumulator columns are two buffers of 128 or one of 256; eight epilogue warps
 // drain a buffer while the copies, and with two buffers the products, of the next tile run.
-// 4096 x 8192 x 2048 bf16 takes 31.0 us (4.4 PFLOP/s; the first form, of single CTAs, 133): a
-// stage's products keep the tensor cores busy for 512 cycles of about 560, and a tile's drain into
-// registers is not hidden.
+// 4096 x 8192 x 2048 bf16 takes 33.5 us (4.1 PFLOP/s; the first form, of single CTAs, 133).  With K = 1024, 4096
+// and 8192 it is 24.1, 55.1 and 99.1: a stage (28 to a pair and 1024 of K) takes 0.34 to 0.39 us, 650 to 760 cycles at
+// 1.965 GHz, of which its products fill 512.  Probably the feed bounds it: 35 KB a stage into every SM are 13 TB/s
+// from L2.  The other 12 to 15 us are the launch, the first stages and the drains of seven tiles into registers,
+// which are not hidden.  In a loop of half a second the power cap takes the clock to 1.7 GHz: 36.8 us.
 template <int kN>
 struct PairTile {
     static constexpr int kBuffers = 256 / kN;
@@ -653,7 +658,7 @@ constexpr int kPairThreads = 64 + 256 + 32;  // producer, MMA issuer, two groups
 struct alignas(64) Mx4PairKernel {
     CUtensorMap tm_a, tm_w;    // bytes [rows, K / 2], boxes of 128 and kN / 2 rows x 128 bytes
     CUtensorMap tm_sa, tm_sw;  // scale tiles as [tiles, 128] words, boxes of two tiles
-    CUtensorMap tm_out;        // bf16 (box 64 x 128) or fp32 (32 x 128) [M, N]
+    CUtensorMap tm_out;        // bf16 (box 64 columns x 32 rows) or fp32 (32 x 32) [M, N]
     uint8_t* out_codes;        // kOutGeluMx4
     uint8_t* out_scales;
     int32_t M, N, K;
@@ -1050,7 +1055,7 @@ cudaError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, i
 }
 
 Mx4Plan mx4_plan(int32_t M, int32_t N, int32_t K) {
-    // Which kernel, from sizes alone (us a product, K = 2048 unless said):
+    // Which kernel, from sizes alone (us a product [L2], K = 2048 unless said):
     //  * more 256 x 128 tiles than pairs: 256 x 256 tiles (96 tiles: 8.6, with 128 columns 10.2, single
     //    CTAs 14.7; a block on 4096 rows of 2048: 70, with 128 columns 83);
     //  * fewer: 256 x 128 tiles (64 tiles: 7.0, single CTAs 8.2), unless splitting K makes up for it, which takes
