@@ -1,6 +1,8 @@
 """CPU checks of the entry points around the feed-forward block: argument refusals (before any launch,
 so they run with or without a GPU), workspace and scale sizes, and the plain 64-bit restatements that the
 GPU tests compare with."""
+import types
+
 import pytest
 import torch
 
@@ -172,6 +174,16 @@ def test_binding_rejects_before_any_call(L):
                  lambda: dg.dg_mx4_matmul((x, x), (x, x)), lambda: dg.dg_ffw_mx4(x, (x, x), (x, x))):
         with pytest.raises(ValueError, match="CUDA tensors only"):
             call()
+
+
+def test_binding_rejects_streams_and_tensors_of_another_device():
+    with pytest.raises(ValueError, match="the stream is on device 1, the tensors are on device 0"):
+        dg._On(0, types.SimpleNamespace(device_index=1))
+    other = types.SimpleNamespace(is_cuda=True, device="cuda:1", dtype=torch.float32, shape=torch.Size([4, 8]), get_device=lambda: 1)
+    with pytest.raises(ValueError, match="w_pre is on cuda:1, another device"):
+        dg._arg(other, "w_pre", 0, other.dtype, other.shape)
+    with pytest.raises(ValueError, match="y is on cuda:1, another device"):
+        dg._rows_arg(other, "y", 0, other.dtype, other.shape)
 
 
 # ------------------------------------------------------------------------------------ the restatements themselves
